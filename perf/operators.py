@@ -204,8 +204,9 @@ def _mul32(constant, x):
 
 
 def _draws(n, t, seed):
-    """16-bit draws of elements 0 .. n-1: Philox4x32-10 with key ``seed`` and
-    counter (i // 8, t); element i takes half i % 2 of word (i // 2) % 4."""
+    """16-bit draws of elements 0 .. n-1 (positions in the codes): Philox4x32-10
+    with key ``seed`` and counter (i // 8, t); element i takes half i % 2 of
+    word (i // 2) % 4."""
     c0 = torch.arange(-(-n // 8), device="cuda", dtype=torch.int64)
     c1, c2, c3 = c0 >> 32, torch.full_like(c0, t & 0xFFFFFFFF), torch.full_like(c0, t >> 32)
     c0 = c0 & 0xFFFFFFFF
@@ -236,7 +237,7 @@ def _plain_momentum(s):
     y = (m.view(-1, BLOCK) * inverse[:, None]).clamp_(-level, level).view(s["count"], -1)
     # floor(y + r / 65536) in whole numbers: y * 65536 is exact
     whole = torch.floor(y[:, :size] * 65536.0).to(torch.int64)
-    whole += _draws(s["count"] * size, s["t"], s["seed"]).view(s["count"], size)
+    whole += _draws(blocks * BLOCK, s["t"], s["seed"]).view(s["count"], -1)[:, :size]
     q = torch.zeros_like(y)
     q[:, :size] = (whole >> 16).float()
     s["held"][256:256 + 4 * blocks].view(torch.float32).copy_(scale)
@@ -364,7 +365,7 @@ def exact(case, seed):
     new = beta * old + g
     u = g + beta * new if case["nesterov"] else new
     del old, scale, raw, signed
-    draws = _exact_draws(count * size, s["t"], s["seed"]).view(count, size)
+    draws = _exact_draws(blocks * BLOCK, s["t"], s["seed"]).view(count, -1)[:, :size]
     back = torch.empty_like(new)
     for i in range(count):
         line = torch.zeros(per * BLOCK, dtype=torch.float64, device="cuda")
