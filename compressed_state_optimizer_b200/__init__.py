@@ -12,8 +12,8 @@ there is no CPU fallback.
 """
 from __future__ import annotations
 
-from .binding import (MUA_STATUS_NONFINITE, MicroAdam, MuaError, Layout, library,
-                      library_path, strerror)
+from .binding import (MUA_STATUS_NONFINITE, MUA_STATUS_TIMEOUT, Layout, MicroAdam, MuaError, Muon,
+                      MuonLayout, library, library_path, strerror)
 
-__all__ = ["MicroAdam", "MuaError", "Layout", "library", "library_path", "strerror",
-           "MUA_STATUS_NONFINITE"]
+__all__ = ["MicroAdam", "Muon", "MuaError", "Layout", "MuonLayout", "library", "library_path",
+           "strerror", "MUA_STATUS_NONFINITE", "MUA_STATUS_TIMEOUT"]

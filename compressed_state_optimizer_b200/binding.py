@@ -22,6 +22,8 @@ MUA_ERR_ALIGN = -3
 MUA_ERR_CUDA = -4
 MUA_STATUS_NONFINITE = 1
 MUA_STATUS_TIMEOUT = 2
+MUA_F32 = 0
+MUA_BF16 = 1
 
 # Every symbol include/mua.h declares, with its ctypes signature.
 _P = ctypes.c_void_p
@@ -48,6 +50,22 @@ SIGNATURES = {
     "mua_apply_bf16": (ctypes.c_int, [_P, _P, _P, _P, _f32, _f32, _f32, _f32, _f32, _i64, _u64,
                                       _P, _P, _P]),
     "mua_set_wait_limit_ns": (ctypes.c_int, [_P, _i64]),
+    "mua_muon_create": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_f32),
+                                       ctypes.POINTER(_P)]),
+    "mua_muon_destroy": (None, [_P]),
+    "mua_muon_state_bytes": (_i64, [_P]),
+    "mua_muon_workspace_bytes": (_i64, [_P]),
+    "mua_muon_state_layout": (ctypes.c_int, [_P, ctypes.POINTER(_i64)]),
+    "mua_muon_momentum": (ctypes.c_int, [_P, _P, _i32, _P, _P, _i32, _f32, _i32, _i64, _u64, _P]),
+    "mua_muon_read": (ctypes.c_int, [_P, _P, _P, _i32, _P]),
+    "mua_muon_write": (ctypes.c_int, [_P, _P, _i32, _P, _P]),
+    "mua_muon_orthogonalize": (ctypes.c_int, [_P, _P, _i32, _i64, _i64, _P, _i64, _i64, _P, _f32,
+                                              _P]),
+    "mua_muon_step": (ctypes.c_int, [_P, _P, _i32, _P, _i32, _P, _P, _f32, _f32, _f32, _i32, _f32,
+                                     _f32, _i64, _u64, _P]),
+    "mua_muon_set_wait_limit_ns": (ctypes.c_int, [_P, _i64]),
+    "mua_muon_get_status": (ctypes.c_int, [_P, _P, _P, ctypes.POINTER(ctypes.c_int32)]),
+    "mua_muon_last_cuda_error": (ctypes.c_char_p, []),
     "mua_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "mua_last_cuda_error": (ctypes.c_char_p, []),
     "mua_version": (ctypes.c_char_p, []),
@@ -60,7 +78,9 @@ class MuaError(RuntimeError):
     def __init__(self, code: int, what: str):
         msg = f"{what}: {strerror(code)} ({code})"
         if code == MUA_ERR_CUDA:
-            msg += f" [{library().mua_last_cuda_error().decode()}]"
+            last = (library().mua_muon_last_cuda_error if what.startswith("mua_muon")
+                    else library().mua_last_cuda_error)
+            msg += f" [{last().decode()}]"
         super().__init__(msg)
         self.code = code
 
@@ -245,4 +265,198 @@ class MicroAdam:
         out = ctypes.c_int32()
         _check(library().mua_get_status(self._h, state.data_ptr(), _stream_ptr(stream),
                                         ctypes.byref(out)), "mua_get_status")
+        return int(out.value)
+
+
+@dataclass
+class MuonLayout:
+    header: int
+    scales: int
+    codes: int
+    blocks: int
+    bytes: int
+
+
+class Muon:
+    """One Muon problem: ``count`` matrices of ``rows x cols`` one after the
+    other, their momentum held in ``bits`` = 8 or 4 bits per value, the update
+    orthogonalised by ``steps`` Newton-Schulz products.
+
+    ``coefficients``: (a, b, c) of the polynomial a + b x + c x^2 of every step,
+    or a sequence of ``steps`` of them; default (3.4445, -4.7750, 2.0315).
+
+    The state and the workspace are caller-owned ``torch.uint8`` tensors (see
+    :meth:`new_state` and :meth:`new_workspace`). A workspace serves one call
+    at a time; calls on several streams, or captured graphs that may overlap,
+    take one each. None of this is differentiable: tensors that would record a
+    gradient are refused, except the parameters ``step`` updates in place.
+    """
+
+    def __init__(self, rows: int, cols: int, count: int = 1, *, bits: int = 8, steps: int = 5,
+                 coefficients=None):
+        lib = library()
+        arr = None
+        if coefficients is not None:
+            c = list(coefficients)
+            if len(c) == 3 and not hasattr(c[0], "__len__"):
+                c = [c] * steps
+            if len(c) != steps or any(len(x) != 3 for x in c):
+                raise ValueError("coefficients: one (a, b, c), or one for each step")
+            arr = (_f32 * (3 * steps))(*[float(v) for x in c for v in x])
+        h = ctypes.c_void_p()
+        _check(lib.mua_muon_create(rows, cols, count, bits, steps, arr, ctypes.byref(h)),
+               "mua_muon_create")
+        self._h = h
+        self.rows, self.cols, self.count = rows, cols, count
+        self.bits, self.steps = bits, steps
+        self.d = rows * cols * count
+        self.state_bytes = int(lib.mua_muon_state_bytes(h))
+        self.workspace_bytes = int(lib.mua_muon_workspace_bytes(h))
+        out = (ctypes.c_int64 * 5)()
+        _check(lib.mua_muon_state_layout(h, out), "mua_muon_state_layout")
+        self.layout = MuonLayout(*[int(x) for x in out])
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and _lib is not None:
+            _lib.mua_muon_destroy(h)
+            self._h = None
+
+    # ------------------------------------------------------------ buffers
+    def new_state(self, device="cuda"):
+        import torch
+        return torch.zeros(self.state_bytes, dtype=torch.uint8, device=device)
+
+    def new_workspace(self, device="cuda"):
+        import torch
+        w = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+        w[:256].zero_()
+        return w
+
+    # ------------------------------------------------------------ checks
+    @staticmethod
+    def _type(x, what):
+        import torch
+        if x.dtype == torch.float32:
+            return MUA_F32
+        if x.dtype == torch.bfloat16:
+            return MUA_BF16
+        raise ValueError(f"{what}: float32 or bfloat16, not {x.dtype}")
+
+    def _values(self, x, what):
+        """A contiguous tensor of all count * rows * cols values."""
+        if x.numel() != self.d or not x.is_contiguous():
+            raise ValueError(f"{what}: {self.d} contiguous values, not shape {tuple(x.shape)} "
+                             f"with strides {tuple(x.stride())}")
+        return self._type(x, what)
+
+    def _buffer(self, x, size, what):
+        import torch
+        if x.dtype != torch.uint8 or not x.is_contiguous() or x.numel() < size:
+            raise ValueError(f"{what}: a contiguous uint8 tensor of at least {size} bytes")
+
+    def _stack(self, x, what):
+        """(matrix stride, row stride) of a [count, rows, cols] view."""
+        shape = (self.count, self.rows, self.cols)
+        if tuple(x.shape) != shape and not (self.count == 1 and tuple(x.shape) == shape[1:]):
+            raise ValueError(f"{what}: shape {shape}, not {tuple(x.shape)}")
+        if self.cols > 1 and x.stride(-1) != 1:
+            raise ValueError(f"{what}: columns must be contiguous")
+        row = x.stride(-2) if self.rows > 1 else self.cols
+        return (x.stride(0) if self.count > 1 else self.rows * row), row
+
+    @staticmethod
+    def _device(stream, *tensors, params=None):
+        """The tensors' CUDA device and the stream's pointer on it."""
+        import torch
+        dev = tensors[0].device
+        for x in tensors:
+            if not x.is_cuda or x.device != dev:
+                raise ValueError("tensors must be on one CUDA device")
+            if x.requires_grad and torch.is_grad_enabled() and x is not params:
+                raise ValueError("not differentiable: detach() the tensors")
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+        return torch.cuda.device(dev), stream.cuda_stream
+
+    # ------------------------------------------------------------ operators
+    def momentum(self, grads, state, direction, *, beta, nesterov=True, t, seed, stream=None):
+        """The momentum update of step ``t``: ``grads`` (fp32 or bf16) into
+        ``state``, the direction to ``direction`` (fp32 or bf16)."""
+        gt, dt = self._values(grads, "grads"), self._values(direction, "direction")
+        self._buffer(state, self.state_bytes, "state")
+        device, s = self._device(stream, grads, state, direction)
+        with device:
+            _check(library().mua_muon_momentum(self._h, grads.data_ptr(), gt, state.data_ptr(),
+                                               direction.data_ptr(), dt, beta, int(nesterov), t,
+                                               seed, s), "mua_muon_momentum")
+
+    def read_momentum(self, state, out, stream=None):
+        """The momentum's values to ``out`` (fp32 or bf16)."""
+        ot = self._values(out, "out")
+        self._buffer(state, self.state_bytes, "state")
+        device, s = self._device(stream, state, out)
+        with device:
+            _check(library().mua_muon_read(self._h, state.data_ptr(), out.data_ptr(), ot, s),
+                   "mua_muon_read")
+
+    def write_momentum(self, values, state, stream=None):
+        """``values`` (fp32 or bf16) as the momentum, each to the nearest level."""
+        vt = self._values(values, "values")
+        self._buffer(state, self.state_bytes, "state")
+        device, s = self._device(stream, values, state)
+        with device:
+            _check(library().mua_muon_write(self._h, values.data_ptr(), vt, state.data_ptr(), s),
+                   "mua_muon_write")
+
+    def orthogonalize(self, x, out, workspace, *, eps=1e-7, stream=None):
+        """Newton-Schulz orthogonalisation of the matrices ``x`` ([count, rows,
+        cols], fp32 or bf16, any matrix and row strides) into ``out`` (bf16,
+        likewise; it may be ``x``)."""
+        import torch
+        xt = self._type(x, "x")
+        xs, xr = self._stack(x, "x")
+        os_, orow = self._stack(out, "out")
+        if out.dtype != torch.bfloat16:
+            raise ValueError(f"out: bfloat16, not {out.dtype}")
+        self._buffer(workspace, self.workspace_bytes, "workspace")
+        device, s = self._device(stream, x, out, workspace)
+        with device:
+            _check(library().mua_muon_orthogonalize(self._h, x.data_ptr(), xt, xs, xr,
+                                                    out.data_ptr(), os_, orow,
+                                                    workspace.data_ptr(), eps, s),
+                   "mua_muon_orthogonalize")
+
+    def step(self, params, grads, state, workspace, *, lr, beta=0.95, eps=1e-7, wd=0.0,
+             scale=None, nesterov=True, t, seed, stream=None):
+        """One full step ``t``: momentum, orthogonalisation, update of
+        ``params`` (fp32 or bf16) by lr * scale, with decoupled weight decay.
+        ``scale`` defaults to sqrt(max(1, rows / cols))."""
+        if scale is None:
+            scale = math.sqrt(max(1.0, self.rows / self.cols))
+        pt, gt = self._values(params, "params"), self._values(grads, "grads")
+        self._buffer(state, self.state_bytes, "state")
+        self._buffer(workspace, self.workspace_bytes, "workspace")
+        device, s = self._device(stream, params, grads, state, workspace, params=params)
+        with device:
+            _check(library().mua_muon_step(self._h, params.data_ptr(), pt, grads.data_ptr(), gt,
+                                           state.data_ptr(), workspace.data_ptr(), lr, scale, beta,
+                                           int(nesterov), eps, wd, t, seed, s), "mua_muon_step")
+
+    def set_wait_limit_ns(self, ns: int):
+        """Bound on a wait inside the matrix-product kernels (<= 0: give up at once)."""
+        _check(library().mua_muon_set_wait_limit_ns(self._h, int(ns)),
+               "mua_muon_set_wait_limit_ns")
+
+    def status(self, buffer, stream=None) -> int:
+        """Status bits of a state (``step``, ``momentum``) or of a workspace
+        (``orthogonalize``)."""
+        self._buffer(buffer, 256, "buffer")
+        device, s = self._device(stream, buffer)
+        out = ctypes.c_int32()
+        with device:
+            _check(library().mua_muon_get_status(self._h, buffer.data_ptr(), s,
+                                                 ctypes.byref(out)), "mua_muon_get_status")
         return int(out.value)

@@ -246,6 +246,135 @@ int mua_set_wait_limit_ns(mua_t h, int64_t ns);
  */
 int mua_get_status(mua_t h, const void* state, void* stream, int32_t* out);
 
+/*
+ * ---------------------------------------------------------------- Muon
+ * A step for matrices: heavy-ball momentum, held in 8 or 4 bits per value, and
+ * an update orthogonalised by Newton-Schulz products (the Muon optimizer).
+ * Per matrix with gradient g and momentum m:
+ *   m' = beta m + g;  U = g + beta m' (nesterov) or m'
+ *   X_0 = U / (|U|_F + eps)
+ *   X_{k+1} = (a_k I + b_k A + c_k A^2) X_k,  A = X_k X_k^T   (k < steps)
+ *   p <- p (1 - lr wd) - lr scale X_steps
+ * (a matrix with rows > cols uses A = X^T X on the right, the same result).
+ *
+ * The momentum: blocks of 128 consecutive values of one row-major matrix (its
+ * last block ragged) share an fp32 scale s; a value is s q, |q| <= L = 127 or
+ * 7. The update writes s' = max|m'| / L and q' = floor(m' / s' + r / 2^16), r
+ * the value's 16-bit Philox4x32-10 draw as in mua_step (element index: block
+ * number * 128 + position, t, seed): unbiased. A block whose largest value is
+ * below 2^-100 is stored as zeros.
+ *
+ * Precision of X: fp16 operands, fp32 sums; about 1e-3 relative to exact
+ * arithmetic in the Frobenius norm.
+ *
+ * The conventions at the top of this header hold. Calls of one handle may run
+ * at once when they use different states and workspaces; a workspace belongs
+ * to one call at a time (captured graphs that share one must not overlap).
+ * Pointers to values need the alignment of their type, states and workspaces
+ * 16 bytes. A NaN or infinity in m' sets MUA_STATUS_NONFINITE in the state and
+ * makes that matrix's results NaN or unspecified; other matrices are not
+ * affected. MUA_ERR_CUDA's text is given by mua_muon_last_cuda_error().
+ */
+#define MUA_F32 0  /* types of values */
+#define MUA_BF16 1
+
+#define MUA_MUON_MAX_STEPS 16
+
+/* Fields written by mua_muon_state_layout(). */
+#define MUA_MUON_LAYOUT_HEADER 0  /* byte offset of the header (status: word 4)      */
+#define MUA_MUON_LAYOUT_SCALES 1  /* byte offset of the fp32 scales, one per block   */
+#define MUA_MUON_LAYOUT_CODES 2   /* byte offset of the codes: int8, or nibbles (two's
+                                     complement, even position in the low nibble)    */
+#define MUA_MUON_LAYOUT_BLOCKS 3  /* blocks of one matrix                            */
+#define MUA_MUON_LAYOUT_BYTES 4   /* total (= mua_muon_state_bytes)                  */
+#define MUA_MUON_LAYOUT_FIELDS 5
+
+typedef struct mua_muon_ctx* mua_muon_t;
+
+/*
+ * mua_muon_create - describe `count` matrices of rows x cols, stored one after
+ * the other. Host only.
+ *   bits          8 or 4 bits per momentum value
+ *   steps         1 .. MUA_MUON_MAX_STEPS Newton-Schulz steps
+ *   coefficients  3 * steps floats (a_k, b_k, c_k), read during the call, or
+ *                 NULL for (3.4445, -4.7750, 2.0315) in every step
+ * Errors: MUA_ERR_ARG for a size or count below 1, a step count out of range or
+ * a coefficient that is not finite; MUA_ERR_UNSUPPORTED for other bits, a side
+ * above 2^20, a shorter side above 2^15, 2^31 or more values in a matrix, or
+ * coefficients under which |X| could pass 1024 for singular values in [0, 1].
+ */
+int mua_muon_create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t steps,
+                    const float* coefficients, mua_muon_t* out);
+
+/* mua_muon_destroy - release a handle (NULL is ignored). Host only. */
+void mua_muon_destroy(mua_muon_t h);
+
+/*
+ * mua_muon_state_bytes / mua_muon_workspace_bytes - sizes of the caller-owned
+ * buffers. The state (header, scales, codes) is zero-filled before the first
+ * step; of the workspace the first 256 bytes are zero-filled once (its status
+ * word), the rest is scratch.
+ */
+int64_t mua_muon_state_bytes(mua_muon_t h);
+int64_t mua_muon_workspace_bytes(mua_muon_t h);
+
+/* mua_muon_state_layout - write the MUA_MUON_LAYOUT_FIELDS values above. */
+int mua_muon_state_layout(mua_muon_t h, int64_t* out);
+
+/*
+ * mua_muon_momentum - the momentum update alone: grads (count x rows x cols of
+ * grads_type, contiguous) into the state, and the direction U (contiguous, of
+ * direction_type) out. grads and direction must not overlap (MUA_ERR_ARG).
+ */
+int mua_muon_momentum(mua_muon_t h, const void* grads, int32_t grads_type, void* state,
+                      void* direction, int32_t direction_type, float beta, int32_t nesterov,
+                      int64_t t, uint64_t seed, void* stream);
+
+/*
+ * mua_muon_read / mua_muon_write - the momentum as contiguous values, and back
+ * (each value to its block's nearest level, ties to even: what was read as
+ * fp32 is written as the same codes).
+ */
+int mua_muon_read(mua_muon_t h, const void* state, void* out, int32_t type, void* stream);
+int mua_muon_write(mua_muon_t h, const void* values, int32_t type, void* state, void* stream);
+
+/*
+ * mua_muon_orthogonalize - X_steps of a stack of matrices x, to the bf16 stack
+ * out. Strides count elements; columns are contiguous. x may be broadcast
+ * (stride 0); the rows of out must not overlap. out may be x itself (bf16, the
+ * same strides), but may not overlap it otherwise. eps >= 0. A matrix of zeros
+ * gives zeros; one with a NaN or infinity gives NaN.
+ */
+int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t x_matrix_stride,
+                           int64_t x_row_stride, void* out, int64_t out_matrix_stride,
+                           int64_t out_row_stride, void* workspace, float eps, void* stream);
+
+/*
+ * mua_muon_step - the whole step t (1, 2, ...) on `stream`: params (fp32 or
+ * bf16, contiguous) are updated in place, formed in fp32 and rounded once.
+ * X_steps is not rounded to bf16 on the way.
+ */
+int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* grads,
+                  int32_t grads_type, void* state, void* workspace, float lr, float scale,
+                  float beta, int32_t nesterov, float eps, float wd, int64_t t, uint64_t seed,
+                  void* stream);
+
+/*
+ * mua_muon_set_wait_limit_ns - bound on a wait inside the matrix-product
+ * kernels, as mua_set_wait_limit_ns; a kernel that gives up sets
+ * MUA_STATUS_TIMEOUT and that call's results are unspecified.
+ */
+int mua_muon_set_wait_limit_ns(mua_muon_t h, int64_t ns);
+
+/*
+ * mua_muon_get_status - the sticky status word of a state, or of the workspace
+ * for mua_muon_orthogonalize, as mua_get_status. Synchronizes `stream`.
+ */
+int mua_muon_get_status(mua_muon_t h, const void* buffer, void* stream, int32_t* out);
+
+/* mua_muon_last_cuda_error - the last CUDA error a mua_muon call of this thread saw. */
+const char* mua_muon_last_cuda_error(void);
+
 /* mua_strerror — static text for a return code. */
 const char* mua_strerror(int code);
 
