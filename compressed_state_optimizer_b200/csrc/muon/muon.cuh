@@ -1,5 +1,5 @@
 // Arguments and launchers of the Muon kernels (muon_momentum.cu,
-// muon_gemm.cu) behind the mua_muon_* entry points (muon_api.cu).
+// muon_ns.cu) behind the mua_muon_* entry points (muon_api.cu).
 //
 // One step for a matrix with gradient g and momentum m (held quantized):
 //   m' = beta m + g,  U = g + beta m' (Nesterov) or m'
@@ -26,6 +26,7 @@ constexpr int kMuonBlock = 128;          // values per quantization scale
 constexpr int kMuonMaxSteps = 16;
 constexpr int kMuonMaxParts = 256;       // partial sums of one matrix's norm
 constexpr int kMuonHdrStatus = 4;        // header word, as in the MicroAdam state
+constexpr int kMuonHdrBarrier = 5;       // of the workspace: arrivals at the grid barrier
 constexpr uint32_t kMuonNonFinite = 1u;
 constexpr uint32_t kMuonTimeout = 2u;
 
@@ -67,52 +68,46 @@ cudaError_t muon_launch_direction_norm(const MuonShape& s, const MuonQuant& q, c
                                        cudaStream_t st);
 // X_0 in fp16: x 2^(e0 - t) with 2^(t-1) <= |x|_F + eps < 2^t, an exact scaling;
 // factor[i] = 2^t / (|x|_F + eps) is applied in fp32 by the first products.
+// Both also zero the grid barrier's count.
 cudaError_t muon_launch_load(const MuonShape& s, const MuonView& x, const double* partials,
-                             float eps, int e0, void* X, float* factor, cudaStream_t st);
+                             float eps, int e0, void* X, float* factor, uint32_t* barrier,
+                             cudaStream_t st);
 // The momentum update; direction U to `out` (fp32 or bf16, contiguous), or,
 // with X != NULL, straight to X_0 as in muon_launch_load.
 cudaError_t muon_launch_momentum(const MuonShape& s, const MuonQuant& q, const void* g, int g_type,
                                  float beta, int nesterov, const MuonRandom& rnd, void* out,
                                  int out_type, const double* partials, float eps, int e0, void* X,
-                                 float* factor, cudaStream_t st);
+                                 float* factor, uint32_t* barrier, cudaStream_t st);
 cudaError_t muon_launch_read(const MuonShape& s, const MuonQuant& q, void* out, int out_type,
                              cudaStream_t st);
 cudaError_t muon_launch_write(const MuonShape& s, const MuonQuant& q, const void* values, int type,
                               cudaStream_t st);
 
 // ---------------------------------------------------------------- products
-enum MuonEpilogue : int {
-  kGram = 0,    // A = alpha f^2 X X^T
-  kPoly = 1,    // P = diag I + mid A + alpha A A
-  kUpdate = 2,  // X' = alpha f P X, fp16
-  kOut = 3,     // alpha f P X to a bf16 stack
-  kParams = 4,  // p <- p decay - alpha f (P X)
+// The iteration of one group of matrices, X_0 being in the stack's x[0].
+struct MuonStack {
+  void* x[2];                  // fp16 [batch][rows][ld], the steps alternate
+  void *a, *p;                 // fp16 [batch][s][lds], s the short side
+  int32_t ld, lds;
 };
 
-struct MuonGemm {
-  int32_t M, N, K, batch;      // D [M x N] per matrix
-  int32_t tiles_m, tiles_n, tiles;  // tiles: of one matrix
-  float alpha, mid, diag, decay;
-  const float* factor;         // per matrix, NULL: 1
-  const void* addend;          // A (kPoly)
-  void* out;                   // fp16 [batch][M][ldo], or the caller's stack
+struct MuonNs {
+  int32_t rows, cols, batch, steps;
+  // Power-of-two scales and coefficients of each step's products.
+  float gram_alpha[kMuonMaxSteps];
+  float poly_alpha[kMuonMaxSteps], poly_mid[kMuonMaxSteps], poly_diag[kMuonMaxSteps];
+  float update_alpha[kMuonMaxSteps];  // of the last: lr scale, or the result's
+  const float* factor;         // per matrix, applied in step 0
+  // The last product: result (bf16) or parameters p <- p decay - alpha x.
+  void* out;
   int64_t ldo, batch_stride;   // in elements
-  int32_t out_type;            // of kOut / kParams
-  int32_t out_vec;             // 16-byte accesses allowed on the caller's stack
+  int32_t params, out_type, out_vec;
+  float decay;
+  uint32_t* barrier;           // arrivals at the grid barrier, 0 at the launch
   uint32_t* status;
   uint64_t wait_ns;            // longest wait inside the kernel before it gives up
 };
 
-struct MuonOperand {
-  void* p;                     // fp16 [batch][rows][ld]
-  int32_t rows, cols, ld;
-};
-
-// D = op(A) op(B): an operand whose contraction index is contiguous ("K-major")
-// or whose M / N index is (`mn`).
-cudaError_t muon_launch_gemm(const MuonOperand& a, bool a_mn, const MuonOperand& b, bool b_mn,
-                             int epilogue, MuonGemm g, cudaStream_t st);
-
-int muon_sm_count(cudaError_t* e);
+cudaError_t muon_launch_ns(const MuonStack& m, const MuonNs& g, cudaStream_t st);
 
 }  // namespace mua

@@ -3,8 +3,8 @@
 // A handle holds geometry and the polynomial's plan only. A step runs the
 // stack in groups of matrices (their X, A and P together stay near the L2's
 // size) and enqueues, per group: the norm of the direction, the momentum update
-// with X_0, then three products per Newton-Schulz step, the last one updating
-// the parameters. No device memory is allocated and nothing is synchronized.
+// with X_0, and the Newton-Schulz steps in one launch whose last product
+// updates the parameters. No device memory is allocated and nothing is synchronized.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -118,7 +118,7 @@ mua::MuonRandom random_keys(const mua_muon_ctx* h, int32_t first, int64_t t, uin
 }
 
 struct Target {  // where the last product goes
-  int epilogue;
+  bool params;
   void* out;
   int type;
   int64_t matrix_stride, row_stride;
@@ -126,75 +126,53 @@ struct Target {  // where the last product goes
   float decay;
 };
 
+uint32_t* barrier_word(uint8_t* ws) {
+  return reinterpret_cast<uint32_t*>(ws) + mua::kMuonHdrBarrier;
+}
+
 // The Newton-Schulz steps of matrices first .. first + count - 1, X_0 and its
 // factors being in the workspace.
 int iterate(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count, const Target& to,
             uint32_t* status, cudaStream_t st) {
-  using namespace mua;
-  void* X[2] = {ws + h->off_x[0], ws + h->off_x[1]};
-  void *A = ws + h->off_a, *P = ws + h->off_p;
-  const float* factor = reinterpret_cast<const float*>(ws + h->off_factor);
-  const MuonOperand opA = {A, h->s, h->s, h->lds}, opP = {P, h->s, h->s, h->lds};
-  const int32_t l = h->tall ? h->rows : h->cols;
-  MuonGemm base;
-  std::memset(&base, 0, sizeof base);
-  base.batch = count;
-  base.status = status;
-  base.wait_ns = (uint64_t)std::max<int64_t>(0, h->wait_ns);
+  mua::MuonStack m;
+  m.x[0] = ws + h->off_x[0];
+  m.x[1] = ws + h->off_x[1];
+  m.a = ws + h->off_a;
+  m.p = ws + h->off_p;
+  m.ld = h->ld;
+  m.lds = h->lds;
+  mua::MuonNs g;
+  std::memset(&g, 0, sizeof g);
+  g.rows = h->rows;
+  g.cols = h->cols;
+  g.batch = count;
+  g.steps = h->steps;
   for (int k = 0; k < h->steps; ++k) {
-    const MuonOperand opX = {X[k & 1], h->rows, h->cols, h->ld};
     const int ex = h->ex[k], ea = h->ea[k], ep = h->ep[k];
-    MuonGemm g = base;
-    g.M = g.N = h->s;
-    g.K = l;
-    g.alpha = (float)std::ldexp(1.0, ea - 2 * ex);
-    g.factor = k == 0 ? factor : nullptr;
-    g.out = A;
-    g.ldo = h->lds;
-    g.batch_stride = (int64_t)h->s * h->lds;
-    cudaError_t e = muon_launch_gemm(opX, h->tall, opX, h->tall, kGram, g, st);
-    if (e != cudaSuccess) return fail(e, "Gram product");
-
-    g = base;
-    g.M = g.N = g.K = h->s;
-    g.alpha = (float)std::ldexp((double)h->coef[k][2], ep - 2 * ea);
-    g.mid = (float)std::ldexp((double)h->coef[k][1], ep - ea);
-    g.diag = (float)std::ldexp((double)h->coef[k][0], ep);
-    g.addend = A;
-    g.out = P;
-    g.ldo = h->lds;
-    g.batch_stride = (int64_t)h->s * h->lds;
-    e = muon_launch_gemm(opA, false, opA, false, kPoly, g, st);
-    if (e != cudaSuccess) return fail(e, "polynomial product");
-
-    g = base;
-    g.M = h->rows;
-    g.N = h->cols;
-    g.K = h->s;
-    g.factor = k == 0 ? factor : nullptr;
-    int epilogue = kUpdate;
-    if (k + 1 < h->steps) {
-      g.alpha = (float)std::ldexp(1.0, h->ex[k + 1] - ep - ex);
-      g.out = X[(k + 1) & 1];
-      g.ldo = h->ld;
-      g.batch_stride = (int64_t)h->rows * h->ld;
-    } else {
-      const int64_t size = type_size(to.type);
-      epilogue = to.epilogue;
-      g.alpha = (float)std::ldexp(to.alpha, -ep - ex);
-      g.decay = to.decay;
-      g.out = static_cast<uint8_t*>(to.out) + (int64_t)first * to.matrix_stride * size;
-      g.out_type = to.type;
-      g.ldo = to.row_stride;
-      g.batch_stride = to.matrix_stride;
-      g.out_vec = aligned(g.out, 16) && (to.row_stride * size) % 16 == 0 &&
-                  (count == 1 || (to.matrix_stride * size) % 16 == 0);
-    }
-    e = h->tall ? muon_launch_gemm(opX, false, opP, false, epilogue, g, st)
-                : muon_launch_gemm(opP, false, opX, true, epilogue, g, st);
-    if (e != cudaSuccess) return fail(e, "update product");
+    const bool last = k + 1 == h->steps;
+    g.gram_alpha[k] = (float)std::ldexp(1.0, ea - 2 * ex);
+    g.poly_alpha[k] = (float)std::ldexp((double)h->coef[k][2], ep - 2 * ea);
+    g.poly_mid[k] = (float)std::ldexp((double)h->coef[k][1], ep - ea);
+    g.poly_diag[k] = (float)std::ldexp((double)h->coef[k][0], ep);
+    g.update_alpha[k] = (float)(last ? std::ldexp(to.alpha, -ep - ex)
+                                     : std::ldexp(1.0, h->ex[k + 1] - ep - ex));
   }
-  return MUA_OK;
+  const int64_t size = type_size(to.type);
+  g.factor = reinterpret_cast<const float*>(ws + h->off_factor);
+  g.out = static_cast<uint8_t*>(to.out) + (int64_t)first * to.matrix_stride * size;
+  g.ldo = to.row_stride;
+  g.batch_stride = to.matrix_stride;
+  g.params = to.params;
+  g.out_type = to.type;
+  // Four columns at a time: 16 bytes of fp32, 8 of bf16.
+  g.out_vec = aligned(g.out, 4 * size) && to.row_stride % 4 == 0 &&
+              (count == 1 || to.matrix_stride % 4 == 0);
+  g.decay = to.decay;
+  g.barrier = barrier_word(ws);
+  g.status = status;
+  g.wait_ns = (uint64_t)std::max<int64_t>(0, h->wait_ns);
+  const cudaError_t e = mua::muon_launch_ns(m, g, st);
+  return e == cudaSuccess ? MUA_OK : fail(e, "Newton-Schulz kernel launch");
 }
 
 int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t steps,
@@ -317,7 +295,7 @@ int mua_muon_momentum(mua_muon_t h, const void* grads, int32_t grads_type, void*
   const cudaError_t e = mua::muon_launch_momentum(
       shape(h, h->count), quant(h, state, 0), grads, grads_type, beta, nesterov != 0,
       random_keys(h, 0, t, seed), direction, direction_type, nullptr, 0.0f, 0, nullptr, nullptr,
-      static_cast<cudaStream_t>(stream));
+      nullptr,      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MUA_OK : fail(e, "momentum kernel launch");
 }
 
@@ -355,7 +333,7 @@ int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   double* partials = reinterpret_cast<double*>(ws + h->off_partials);
-  const Target to = {mua::kOut, out, MUA_BF16, out_matrix_stride, out_row_stride, 1.0, 0.0f};
+  const Target to = {false, out, MUA_BF16, out_matrix_stride, out_row_stride, 1.0, 0.0f};
   for (int32_t first = 0; first < h->count; first += h->group) {
     const int32_t count = std::min(h->group, h->count - first);
     const mua::MuonView v = {
@@ -364,7 +342,7 @@ int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t 
     cudaError_t e = mua::muon_launch_norm(shape(h, count), v, partials, st);
     if (e != cudaSuccess) return fail(e, "norm kernel launch");
     e = mua::muon_launch_load(shape(h, count), v, partials, eps, h->ex[0], ws + h->off_x[0],
-                              reinterpret_cast<float*>(ws + h->off_factor), st);
+                              reinterpret_cast<float*>(ws + h->off_factor), barrier_word(ws), st);
     if (e != cudaSuccess) return fail(e, "load kernel launch");
     const int rc = iterate(h, ws, first, count, to,
                            reinterpret_cast<uint32_t*>(ws) + mua::kMuonHdrStatus, st);
@@ -390,7 +368,7 @@ int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* g
   double* partials = reinterpret_cast<double*>(ws + h->off_partials);
   float* factor = reinterpret_cast<float*>(ws + h->off_factor);
   const int64_t n = (int64_t)h->rows * h->cols;
-  const Target to = {mua::kParams, params, params_type, n, h->cols,
+  const Target to = {true, params, params_type, n, h->cols,
                      (double)lr * (double)scale, (float)(1.0 - (double)lr * (double)wd)};
   for (int32_t first = 0; first < h->count; first += h->group) {
     const int32_t count = std::min(h->group, h->count - first);
@@ -402,7 +380,7 @@ int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* g
     if (e != cudaSuccess) return fail(e, "direction norm kernel launch");
     e = mua::muon_launch_momentum(s, q, g, grads_type, beta, nesterov != 0,
                                   random_keys(h, first, t, seed), nullptr, 0, partials, eps,
-                                  h->ex[0], ws + h->off_x[0], factor, st);
+                                  h->ex[0], ws + h->off_x[0], factor, barrier_word(ws), st);
     if (e != cudaSuccess) return fail(e, "momentum kernel launch");
     const int rc = iterate(h, ws, first, count, to,
                            static_cast<uint32_t*>(state) + mua::kMuonHdrStatus, st);

@@ -1,0 +1,863 @@
+// The Newton-Schulz iteration of a stack of matrices in one launch, on the
+// tensor cores (tcgen05.mma, fp16 operands, fp32 accumulators in TMEM).
+//
+// Three products per step, each with its epilogue fused, a grid barrier between:
+//   A  = f^2 X X^T          symmetric: lower block triangle only
+//   P  = a I + b A + c A A  likewise, the polynomial formed in the epilogue
+//   X' = f P X              (X P for a tall matrix); the last one writes the
+//                           result or updates the parameters instead
+// X keeps the caller's orientation: an operand is read with its contraction
+// index contiguous ("K-major") or with its M / N index contiguous, whichever
+// the row-major copy has, so nothing is transposed. A and P hold only the
+// blocks on and below the diagonal; a block above it is read as its mirror
+// block with the other major, so no product writes a mirror image.
+//
+// A tile is 256 x 256 on a pair of CTAs (cta_group::2: each SM holds half of
+// both operands, 8 KB of shared memory read per 16-deep MMA and SM instead of
+// 12) or 128 x 128 on one CTA when the 256-wide tiles would be too few for the
+// SMs. Per CTA: warp 0 streams 64-deep operand slices into a ring of 128-byte
+// swizzled shared tiles (TMA), warp 1 issues the MMAs, warps 2..5 turn
+// finished accumulators into output while the next tile's MMAs run into the
+// other half of TMEM.
+//
+// Every wait is bounded by the global timer. A wait that runs out sets
+// MUA_STATUS_TIMEOUT, the CTA's roles stop, copies and MMAs in flight are
+// awaited (bounded again), TMEM is freed and the kernel returns.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "muon.cuh"
+
+namespace mua {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kEpilogueWarps = 4;
+constexpr int kStages = 6;
+constexpr int kStageBytes = 32768;           // 128 rows of A and of B, 64 deep
+constexpr int kChunkBytes = 4096;            // 32 rows x 64 fp16 columns of output
+constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * 2 * kChunkBytes + 1024;
+constexpr uint64_t kDrainNs = 2000000000ull;  // bound on waits for copies and MMAs in flight
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// False when the wait ran out, or another role of the CTA has given up.
+// A limit of 0 gives up as soon as it would wait.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit,
+                                          volatile uint32_t* stop) {
+  if (mbar_try(bar, parity)) return true;
+  const uint64_t t0 = now_ns();
+  while (limit == 0 || !mbar_try(bar, parity)) {
+    if (*stop) return false;
+    if (limit == 0 || now_ns() - t0 > limit) {
+      *stop = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// A wait for work in flight that other roles' giving up does not end.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = now_ns();
+  while (!mbar_try(bar, parity) && now_ns() - t0 <= kDrainNs) {
+  }
+}
+// A 64 x `rows` box into this CTA's shared memory. With CG = 2 the barrier may
+// be the pair's other CTA's.
+template <int CG>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                         int y, int z) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y,
+                                          int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+               ::"l"(map), "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// At most N stores of this thread still read their shared memory.
+template <int N>
+__device__ __forceinline__ void tma_store_read_wait() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// Orders this thread's acquired view of global memory before its TMA copies.
+__device__ __forceinline__ void fence_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_expect_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
+                   bar),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Shared-memory operand descriptor, 128-byte swizzle. K-major: 8-row groups
+// 1024 bytes apart. M/N-major: 64-element chunks 8192 bytes apart, 8-deep
+// groups of the contraction index 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
+  const uint64_t lead = mn ? 8192 >> 4 : 1;
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (lead << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// fp16 operands, fp32 accumulators, M = 128 per CTA.
+template <int CG, int BN>
+__device__ __forceinline__ uint32_t instruction_desc(bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(BN / 8) << 17) | ((uint32_t)(CG * 128 / 16) << 24);
+}
+template <int CG>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        bool accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// Arrives on the barrier (of both CTAs of a pair) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_load_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+struct Maps {
+  CUtensorMap load_x[2], load_a, load_p;     // boxes of 64 x 64
+  CUtensorMap store_x[2], store_a, store_p;  // 64 x 32
+};
+
+enum Product : int { kGram = 0, kPoly = 1, kUpdate = 2 };
+
+// One product of the iteration: output tiles and contraction length.
+struct Phase {
+  int step, kind, tm, tn, kblocks;
+  int64_t tiles;  // of the whole stack
+};
+template <int CG, int BN>
+__device__ __forceinline__ Phase phase_of(const MuonNs& g, int ph) {
+  Phase p;
+  p.step = ph / 3;
+  p.kind = ph - 3 * p.step;
+  const int s = min(g.rows, g.cols), l = max(g.rows, g.cols);
+  if (p.kind == kUpdate) {
+    p.tm = (g.rows + CG * 128 - 1) / (CG * 128);
+    p.tn = (g.cols + BN - 1) / BN;
+    p.tiles = (int64_t)p.tm * p.tn * g.batch;
+  } else {
+    p.tm = p.tn = (s + BN - 1) / BN;
+    p.tiles = (int64_t)p.tm * (p.tm + 1) / 2 * g.batch;
+  }
+  p.kblocks = ((p.kind == kGram ? l : s) + 63) / 64;
+  return p;
+}
+// Tile t: matrix, row tile, column tile. The triangle is walked row by row;
+// the update walks the short side's tiles first, so that tiles in flight share
+// their slice of X.
+__device__ __forceinline__ void tile_of(const MuonNs& g, const Phase& p, int64_t t, int& z, int& i,
+                                        int& j) {
+  const int per = p.kind == kUpdate ? p.tm * p.tn : p.tm * (p.tm + 1) / 2;
+  z = (int)(t / per);
+  const int r = (int)(t - (int64_t)z * per);
+  if (p.kind == kUpdate) {
+    if (g.rows <= g.cols) {
+      j = r / p.tm;
+      i = r - j * p.tm;
+    } else {
+      i = r / p.tn;
+      j = r - i * p.tn;
+    }
+  } else {
+    i = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > r) --i;
+    while ((i + 1) * (i + 2) / 2 <= r) ++i;
+    j = r - i * (i + 1) / 2;
+  }
+}
+// Whether slice kb of the operand with M / N block `block` is read with its
+// M / N index contiguous. X has one major per product; A and P (symmetric)
+// are read from below the diagonal.
+template <int BN>
+__device__ __forceinline__ bool reads_mn(const MuonNs& g, int kind, bool a, int block, int kb) {
+  const bool tall = g.rows > g.cols;
+  if (kind == kGram) return tall;
+  const bool symmetric = kind == kPoly || a != tall;
+  if (symmetric) return kb * 64 / BN > block;
+  return !tall;  // X: the B operand of a wide update
+}
+
+// Output rows of one warp (32, one per lane) x 64 columns from accumulators to
+// a swizzled shared tile: the layout of a 128-byte-swizzled TMA store.
+__device__ __forceinline__ uint32_t chunk_address(uint32_t tile, int row, int group) {
+  return tile + row * 128 + ((group ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void st_shared(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
+                                          uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// Four consecutive columns of a caller's row: the result, or the parameters'
+// update formed in fp32 and rounded once.
+__device__ __forceinline__ void write_out(const MuonNs& g, int64_t at, int left, const float (&x)[4],
+                                          float alpha) {
+  if (g.params) {
+    if (g.out_type == kF32) {
+      float* p = static_cast<float*>(g.out) + at;
+      if (g.out_vec && left >= 4) {
+        float4 v = *reinterpret_cast<const float4*>(p);
+        v.x = fmaf(-alpha, x[0], v.x * g.decay);
+        v.y = fmaf(-alpha, x[1], v.y * g.decay);
+        v.z = fmaf(-alpha, x[2], v.z * g.decay);
+        v.w = fmaf(-alpha, x[3], v.w * g.decay);
+        *reinterpret_cast<float4*>(p) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < left) p[e] = fmaf(-alpha, x[e], p[e] * g.decay);
+      }
+    } else {
+      uint16_t* p = static_cast<uint16_t*>(g.out) + at;
+      if (g.out_vec && left >= 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        const float a0 = __uint_as_float(v.x << 16), a1 = __uint_as_float(v.x & 0xFFFF0000u);
+        const float a2 = __uint_as_float(v.y << 16), a3 = __uint_as_float(v.y & 0xFFFF0000u);
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(pack_bf16(fmaf(-alpha, x[0], a0 * g.decay), fmaf(-alpha, x[1], a1 * g.decay)),
+                       pack_bf16(fmaf(-alpha, x[2], a2 * g.decay), fmaf(-alpha, x[3], a3 * g.decay)));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < left) {
+            const float v = __uint_as_float((uint32_t)p[e] << 16);
+            p[e] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(-alpha, x[e], v * g.decay)));
+          }
+      }
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(g.out) + at;
+    if (g.out_vec && left >= 4) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0] * alpha, x[1] * alpha),
+                                                pack_bf16(x[2] * alpha, x[3] * alpha));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) p[e] = __bfloat16_as_ushort(__float2bfloat16_rn(x[e] * alpha));
+    }
+  }
+}
+
+// Waits until every CTA has finished the phases before `ph`.
+__device__ __forceinline__ bool grid_wait(const MuonNs& g, int ph, volatile uint32_t* stop) {
+  const uint32_t want = gridDim.x * (uint32_t)ph;
+  const uint64_t t0 = now_ns();
+  while (true) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(g.barrier) : "memory");
+    if (v >= want) return true;
+    if (*stop) return false;
+    if (g.wait_ns == 0 || now_ns() - t0 > g.wait_ns) {
+      *stop = 1;
+      return false;
+    }
+  }
+}
+
+template <int CG, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
+  constexpr int S = kStages;
+  constexpr uint32_t kTmemCols = 2 * BN;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drained;
+  __shared__ __align__(8) uint64_t addend_full[kEpilogueWarps][2];
+  __shared__ uint32_t tmem_base_s, stop, issued_s, peer_issued_s, epilogue_go;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? (blockIdx.x & 1u) : 0u;
+  const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const int phases = 3 * g.steps;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), CG);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&acc_full[a]), 1);
+      mbar_init(smem_u32(&acc_empty[a]), kEpilogueWarps * CG);
+      for (int w = 0; w < kEpilogueWarps; ++w) mbar_init(smem_u32(&addend_full[w][a]), 1);
+    }
+    mbar_init(smem_u32(&drained), 1);
+    stop = 0;
+    issued_s = peer_issued_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    if constexpr (CG == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&tmem_base_s)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&tmem_base_s)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  fence_after();
+  const uint32_t tmem = tmem_base_s;
+  volatile uint32_t* stop_v = &stop;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t issued = 0;
+      bool ok = true;
+      for (int ph = 0; ok && ph < phases; ++ph) {
+        if (ph > 0 && !grid_wait(g, ph, stop_v)) break;
+        fence_async_global();
+        const Phase p = phase_of<CG, BN>(g, ph);
+        const CUtensorMap* x = &maps.load_x[p.step & 1];
+        const bool tall = g.rows > g.cols;
+        const CUtensorMap* ma = p.kind == kGram ? x : (p.kind == kPoly ? &maps.load_a
+                                                                       : (tall ? x : &maps.load_p));
+        const CUtensorMap* mb = p.kind == kGram ? x : (p.kind == kPoly ? &maps.load_a
+                                                                       : (tall ? &maps.load_p : x));
+        for (int64_t t = first; ok && t < p.tiles; t += stride) {
+          int z, i, j;
+          tile_of(g, p, t, z, i, j);
+          const int a0 = i * CG * 128 + (int)rank * 128;        // this CTA's rows of A
+          const int b0 = j * BN + (int)rank * (BN / CG);        // and of B
+          for (int kb = 0; kb < p.kblocks; ++kb, ++issued) {
+            const int s = (int)(issued % S);
+            if (!mbar_wait(smem_u32(&empty[s]), ((issued / S) & 1u) ^ 1u, g.wait_ns, stop_v)) {
+              ok = false;
+              break;
+            }
+            uint32_t bar = smem_u32(&full[s]);
+            if (CG == 2 && rank != 0) {
+              bar = peer_address(bar, 0);
+              mbar_expect_cluster(bar, kStageBytes);
+            } else {
+              mbar_expect(bar, kStageBytes);
+            }
+            const uint32_t a = ring + s * kStageBytes, b = a + 16384;
+            const bool a_mn = reads_mn<BN>(g, p.kind, true, i, kb);
+            const bool b_mn = reads_mn<BN>(g, p.kind, false, j, kb);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              tma_load<CG>(a + q * 8192, ma, bar, a_mn ? a0 + 64 * q : kb * 64,
+                           a_mn ? kb * 64 : a0 + 64 * q, z);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              tma_load<CG>(b + q * 8192, mb, bar, b_mn ? b0 + 64 * q : kb * 64,
+                           b_mn ? kb * 64 : b0 + 64 * q, z);
+          }
+        }
+      }
+      issued_s = issued;
+      if (CG == 2 && rank != 0)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                         peer_address(smem_u32(&peer_issued_s), 0)),
+                     "r"(issued)
+                     : "memory");
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      uint32_t used = 0, n = 0;
+      bool ok = true;
+      for (int ph = 0; ok && ph < phases; ++ph) {
+        const Phase p = phase_of<CG, BN>(g, ph);
+        for (int64_t t = first; ok && t < p.tiles; t += stride, ++n) {
+          int z, i, j;
+          tile_of(g, p, t, z, i, j);
+          const uint32_t acc = n & 1u;
+          if (!mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1u) ^ 1u, g.wait_ns, stop_v)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint32_t d = tmem + acc * BN;
+          for (int kb = 0; kb < p.kblocks; ++kb, ++used) {
+            const int s = (int)(used % S);
+            if (!mbar_wait(smem_u32(&full[s]), (used / S) & 1u, g.wait_ns, stop_v)) {
+              ok = false;
+              break;
+            }
+            fence_after();
+            const uint32_t a = ring + s * kStageBytes, b = a + 16384;
+            const bool a_mn = reads_mn<BN>(g, p.kind, true, i, kb);
+            const bool b_mn = reads_mn<BN>(g, p.kind, false, j, kb);
+            const uint32_t idesc = instruction_desc<CG, BN>(a_mn, b_mn);
+            const uint64_t da = operand_desc(a, a_mn), db = operand_desc(b, b_mn);
+            const uint64_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16<CG>(d, da + k * sa, db + k * sb, idesc, (kb | k) != 0);
+            mma_commit<CG>(smem_u32(&empty[s]));
+          }
+          if (ok) mma_commit<CG>(smem_u32(&acc_full[acc]));
+        }
+      }
+      // The MMAs in flight end before TMEM and the operands go.
+      if constexpr (CG == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                smem_u32(&drained))
+            : "memory");
+      else
+        mma_commit<1>(smem_u32(&drained));
+      mbar_drain(smem_u32(&drained), 0);
+    }
+  } else {
+    const int quarter = warp & 3;  // the TMEM lanes this warp may read
+    const uint32_t stage = ring + S * kStageBytes + (warp - 2) * 2 * kChunkBytes;
+    uint32_t n = 0, chunk = 0;       // tiles, staged chunks
+    uint32_t asked = 0, parity = 0;  // per buffer: an addend copy in flight, its barrier's phase
+    bool ok = true;
+    for (int ph = 0; ok && ph < phases; ++ph) {
+      const Phase p = phase_of<CG, BN>(g, ph);
+      const bool last = ph == phases - 1;
+      const int M = p.kind == kUpdate ? g.rows : min(g.rows, g.cols);
+      const int N = p.kind == kUpdate ? g.cols : M;
+      const CUtensorMap* out = p.kind == kGram ? &maps.store_a
+                                               : (p.kind == kPoly ? &maps.store_p
+                                                                  : &maps.store_x[(p.step & 1) ^ 1]);
+      if (p.kind == kPoly && first < p.tiles) {
+        if (lane == 0) ok = grid_wait(g, ph, stop_v);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        fence_async_global();
+      }
+      for (int64_t t = first; ok && t < p.tiles; t += stride, ++n) {
+        int z, i, j;
+        tile_of(g, p, t, z, i, j);
+        const int row0 = i * CG * 128 + (int)rank * 128 + quarter * 32;
+        const int chunks = row0 < M ? (min(BN, N - j * BN) + 63) / 64 : 0;
+        const uint32_t acc = n & 1u;
+        // The addend's first chunk on its way while the MMAs run.
+        if (p.kind == kPoly && chunks > 0) {
+          if (lane == 0) {
+            tma_store_read_wait<0>();
+            const uint32_t bar = smem_u32(&addend_full[warp - 2][chunk & 1u]);
+            mbar_expect(bar, kChunkBytes);
+            tma_load<1>(stage + (chunk & 1u) * kChunkBytes, &maps.store_a, bar, j * BN, row0, z);
+          }
+          asked |= 1u << (chunk & 1u);
+        }
+        ok = mbar_wait(smem_u32(&acc_full[acc]), (n >> 1) & 1u, g.wait_ns, stop_v);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN;
+        if (ok) {
+          fence_after();
+          float f = g.factor && p.step == 0 && p.kind != kPoly ? g.factor[z] : 1.0f;
+          if (p.kind == kGram) f *= f;
+          const float alpha = f * (p.kind == kGram ? g.gram_alpha[p.step]
+                                                   : (p.kind == kPoly ? g.poly_alpha[p.step]
+                                                                      : g.update_alpha[p.step]));
+          if (!last) {
+            const float mid = g.poly_mid[p.step], diag = g.poly_diag[p.step];
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c, ++chunk) {
+              const uint32_t tile = stage + (chunk & 1u) * kChunkBytes;
+              uint32_t v[2][32];
+              tmem_load32(lanes + 64 * c, v[0]);
+              tmem_load32(lanes + 64 * c + 32, v[1]);
+              // This buffer's last store has been read; the other's too before the
+              // next addend lands there.
+              if (p.kind == kPoly) {
+                if (c + 1 < chunks) {
+                  const uint32_t next = (chunk + 1) & 1u;
+                  if (lane == 0) {
+                    tma_store_read_wait<0>();
+                    const uint32_t bar = smem_u32(&addend_full[warp - 2][next]);
+                    mbar_expect(bar, kChunkBytes);
+                    tma_load<1>(stage + next * kChunkBytes, &maps.store_a, bar,
+                                j * BN + 64 * (c + 1), row0, z);
+                  }
+                  asked |= 1u << next;
+                }
+                const uint32_t now = chunk & 1u;
+                mbar_drain(smem_u32(&addend_full[warp - 2][now]), (parity >> now) & 1u);
+                asked &= ~(1u << now);
+                parity ^= 1u << now;
+              } else {
+                if (lane == 0) tma_store_read_wait<1>();
+              }
+              __syncwarp();
+              tmem_load_wait();
+              const int diagonal = row0 + lane - (j * BN + 64 * c);  // column of the diagonal
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const uint32_t at = chunk_address(tile, lane, q);
+                uint32_t w[4];
+                if (p.kind == kPoly) {
+                  const uint4 a = ld_shared(at);
+                  const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const __half2 h = *reinterpret_cast<const __half2*>(&aw[e]);
+                    float x0 = __uint_as_float(v[q >> 2][(8 * q + 2 * e) & 31]) * alpha;
+                    float x1 = __uint_as_float(v[q >> 2][(8 * q + 2 * e + 1) & 31]) * alpha;
+                    x0 = fmaf(__low2float(h), mid, x0);
+                    x1 = fmaf(__high2float(h), mid, x1);
+                    if (8 * q + 2 * e == diagonal) x0 += diag;
+                    if (8 * q + 2 * e + 1 == diagonal) x1 += diag;
+                    w[e] = pack_f16(x0, x1);
+                  }
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    w[e] = pack_f16(__uint_as_float(v[q >> 2][(8 * q + 2 * e) & 31]) * alpha,
+                                    __uint_as_float(v[q >> 2][(8 * q + 2 * e + 1) & 31]) * alpha);
+                }
+                st_shared(at, w[0], w[1], w[2], w[3]);
+              }
+              fence_async_shared();
+              __syncwarp();
+              if (lane == 0) tma_store(out, tile, j * BN + 64 * c, row0, z);
+            }
+          } else {
+            if (lane == 0) tma_store_read_wait<0>();
+            __syncwarp();
+            // 32 x 32 fp32 through shared memory: a lane then holds four columns,
+            // eight lanes a row's 128 (64) contiguous bytes.
+#pragma unroll 1
+            for (int c = 0; c < 2 * chunks; ++c) {
+              uint32_t v[32];
+              tmem_load32(lanes + 32 * c, v);
+              tmem_load_wait();
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                st_shared(chunk_address(stage, lane, q), v[4 * q], v[4 * q + 1], v[4 * q + 2],
+                          v[4 * q + 3]);
+              __syncwarp();
+              const int col = j * BN + 32 * c + 4 * (lane & 7);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const int r = 4 * q + (lane >> 3), row = row0 + r;
+                const uint4 u = ld_shared(chunk_address(stage, r, lane & 7));
+                const float x[4] = {__uint_as_float(u.x), __uint_as_float(u.y),
+                                    __uint_as_float(u.z), __uint_as_float(u.w)};
+                if (row < M && col < N)
+                  write_out(g, (int64_t)z * g.batch_stride + (int64_t)row * g.ldo + col, N - col, x,
+                            alpha);
+              }
+              __syncwarp();
+            }
+          }
+        }
+        fence_before();
+        __syncwarp();
+        if (!ok) break;
+        if (lane == 0) {
+          if (CG == 2 && rank != 0)
+            mbar_arrive_cluster(peer_address(smem_u32(&acc_empty[acc]), 0));
+          else
+            mbar_arrive(smem_u32(&acc_empty[acc]));
+        }
+      }
+      // This CTA's output is in memory: tell the grid. One thread decides for
+      // the four warps whether to go on.
+      if (lane == 0) tma_store_wait_all();
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
+      if (warp == 2 && lane == 0) {
+        // A CTA without a tile here must not count ahead of the others.
+        const bool go = !last && grid_wait(g, ph, stop_v) && *stop_v == 0;
+        epilogue_go = go;
+        if (go) {
+          __threadfence();
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.barrier) : "memory");
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
+      ok = epilogue_go != 0;
+    }
+    for (uint32_t b = 0; b < 2; ++b)
+      if (asked >> b & 1u)
+        mbar_drain(smem_u32(&addend_full[warp - 2][b]), (parity >> b) & 1u);
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  // Operand copies land before their shared memory goes. A pair's copies count
+  // on the first CTA's barriers, one arrival from each CTA: where the two gave
+  // up at different slices the missing arrivals are made here.
+  if (threadIdx.x == 0 && rank == 0) {
+    const uint32_t mine = issued_s, other = CG == 2 ? peer_issued_s : mine;
+    const uint32_t most = max(mine, other);
+    for (uint32_t c = min(mine, other); c < most; ++c) mbar_arrive(smem_u32(&full[c % S]));
+    for (uint32_t c = most > S ? most - S : 0; c < most; ++c)
+      mbar_drain(smem_u32(&full[c % S]), (c / S) & 1u);
+  }
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  fence_after();
+  if (warp == 1) {
+    if constexpr (CG == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(kTmemCols));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(kTmemCols));
+  }
+  if constexpr (CG == 2) cluster_sync();
+  if (threadIdx.x == 0 && stop) atomicOr(g.status, kMuonTimeout);
+}
+// ---------------------------------------------------------------- host
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encode_fn(EncodeFn* out) {
+  static EncodeFn fn = nullptr;  // a process-wide driver entry point
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                           cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+    fn = reinterpret_cast<EncodeFn>(p);
+  }
+  *out = fn;
+  return cudaSuccess;
+}
+
+struct Operand {
+  void* p;  // fp16 [batch][rows][ld]
+  int32_t rows, cols, ld;
+};
+
+// Copies of 64 contiguous elements x `box_rows` rows of a batch of row-major
+// matrices; what lies outside a matrix reads as 0 and is not written.
+cudaError_t make_map(const Operand& o, int batch, int box_rows, CUtensorMap* map) {
+  EncodeFn encode;
+  const cudaError_t e = encode_fn(&encode);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)batch};
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.ld * 2 * o.rows};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  const CUresult r =
+      encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, o.p, dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+
+constexpr int kMaxDevices = 64;
+
+// CTAs of a cooperative launch that the current device holds at once.
+template <int CG, int BN>
+cudaError_t resident_ctas(int* out) {
+  static int known[kMaxDevices];  // 0: not asked yet
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && known[dev] > 0) {
+    *out = known[dev];
+    return cudaSuccess;
+  }
+  auto kernel = ns_kernel<CG, BN>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  int n = 0;
+  if (CG == 2) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    n *= 2;
+  } else {
+    int sms = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, kSmem);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    n *= sms;
+  }
+  if (e != cudaSuccess) return e;
+  if (n < CG) return cudaErrorLaunchOutOfResources;
+  if (dev < kMaxDevices) known[dev] = n;
+  *out = n;
+  return cudaSuccess;
+}
+
+template <int CG, int BN>
+cudaError_t run(const Maps& maps, const MuonNs& g, int64_t tiles, cudaStream_t st) {
+  int most = 0;
+  const cudaError_t e = resident_ctas<CG, BN>(&most);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(most, tiles * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, ns_kernel<CG, BN>, maps, g);
+}
+
+int64_t most_tiles(const MuonNs& g, int side) {
+  const int64_t tm = (g.rows + side - 1) / side, tn = (g.cols + side - 1) / side;
+  return tm * tn * g.batch;
+}
+
+}  // namespace
+
+cudaError_t muon_launch_ns(const MuonStack& m, const MuonNs& g, cudaStream_t st) {
+  Maps maps;
+  const int s = std::min(g.rows, g.cols);
+  for (int store = 0; store < 2; ++store) {
+    const int rows = store ? 32 : 64;
+    CUtensorMap* x = store ? maps.store_x : maps.load_x;
+    for (int k = 0; k < 2; ++k) {
+      const cudaError_t e = make_map({m.x[k], g.rows, g.cols, m.ld}, g.batch, rows, &x[k]);
+      if (e != cudaSuccess) return e;
+    }
+    cudaError_t e = make_map({m.a, s, s, m.lds}, g.batch, rows, store ? &maps.store_a : &maps.load_a);
+    if (e == cudaSuccess)
+      e = make_map({m.p, s, s, m.lds}, g.batch, rows, store ? &maps.store_p : &maps.load_p);
+    if (e != cudaSuccess) return e;
+  }
+  // 256-wide tiles on CTA pairs halve the operand traffic; below one tile per
+  // pair the 128-wide ones keep more SMs busy.
+  const int64_t wide = most_tiles(g, 256);
+  if (wide >= 74) return run<2, 256>(maps, g, wide, st);
+  return run<1, 128>(maps, g, most_tiles(g, 128), st);
+}
+
+}  // namespace mua
