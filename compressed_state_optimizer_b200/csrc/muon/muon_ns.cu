@@ -49,6 +49,14 @@ __device__ __forceinline__ uint64_t now_ns() {
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -63,7 +71,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -74,7 +82,10 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // A limit of 0 gives up as soon as it would wait.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit,
                                           volatile uint32_t* stop) {
-  if (mbar_try(bar, parity)) return true;
+  for (int spin = 0; spin < 64; ++spin) {
+    if (mbar_try(bar, parity)) return true;
+    if (limit == 0) break;
+  }
   const uint64_t t0 = now_ns();
   while (limit == 0 || !mbar_try(bar, parity)) {
     if (*stop) return false;
@@ -87,6 +98,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
 }
 // A wait for work in flight that other roles' giving up does not end.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  if (mbar_try(bar, parity)) return;
   const uint64_t t0 = now_ns();
   while (!mbar_try(bar, parity) && now_ns() - t0 <= kDrainNs) {
   }
@@ -137,7 +149,7 @@ __device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {
   return r;
 }
 __device__ __forceinline__ void mbar_expect_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
                    bar),
                "r"(bytes)
                : "memory");
@@ -429,31 +441,36 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
   const uint32_t tmem = tmem_base_s;
   volatile uint32_t* stop_v = &stop;
 
+  // Warps 0 and 1 run their loops converged; an elected lane issues.
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t issued = 0;
-      bool ok = true;
-      for (int ph = 0; ok && ph < phases; ++ph) {
-        if (ph > 0 && !grid_wait(g, ph, stop_v)) break;
-        fence_async_global();
-        const Phase p = phase_of<CG, BN>(g, ph);
-        const CUtensorMap* x = &maps.load_x[p.step & 1];
-        const bool tall = g.rows > g.cols;
-        const CUtensorMap* ma = p.kind == kGram ? x : (p.kind == kPoly ? &maps.load_a
-                                                                       : (tall ? x : &maps.load_p));
-        const CUtensorMap* mb = p.kind == kGram ? x : (p.kind == kPoly ? &maps.load_a
-                                                                       : (tall ? &maps.load_p : x));
-        for (int64_t t = first; ok && t < p.tiles; t += stride) {
-          int z, i, j;
-          tile_of(g, p, t, z, i, j);
-          const int a0 = i * CG * 128 + (int)rank * 128;        // this CTA's rows of A
-          const int b0 = j * BN + (int)rank * (BN / CG);        // and of B
-          for (int kb = 0; kb < p.kblocks; ++kb, ++issued) {
-            const int s = (int)(issued % S);
-            if (!mbar_wait(smem_u32(&empty[s]), ((issued / S) & 1u) ^ 1u, g.wait_ns, stop_v)) {
-              ok = false;
-              break;
-            }
+    uint32_t issued = 0, s = 0, turn = 1;
+    bool ok = true;
+    for (int ph = 0; ok && ph < phases; ++ph) {
+      if (ph > 0) {
+        ok = grid_wait(g, ph, stop_v);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+      }
+      fence_async_global();
+      const Phase p = phase_of<CG, BN>(g, ph);
+      const CUtensorMap* x = &maps.load_x[p.step & 1];
+      const bool tall = g.rows > g.cols;
+      const CUtensorMap* ma = p.kind == kGram ? x : (p.kind == kPoly ? &maps.load_a
+                                                                     : (tall ? x : &maps.load_p));
+      const CUtensorMap* mb = p.kind == kGram ? x : (p.kind == kPoly ? &maps.load_a
+                                                                     : (tall ? &maps.load_p : x));
+      for (int64_t t = first; ok && t < p.tiles; t += stride) {
+        int z, i, j;
+        tile_of(g, p, t, z, i, j);
+        const int a0 = i * CG * 128 + (int)rank * 128;  // this CTA's rows of A
+        const int b0 = j * BN + (int)rank * (BN / CG);  // and of B
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          ok = mbar_wait(smem_u32(&empty[s]), turn, g.wait_ns, stop_v);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          const uint32_t a = ring + s * kStageBytes, b = a + 16384;
+          const bool a_mn = reads_mn<BN>(g, p.kind, true, i, kb);
+          const bool b_mn = reads_mn<BN>(g, p.kind, false, j, kb);
+          if (elect_one()) {
             uint32_t bar = smem_u32(&full[s]);
             if (CG == 2 && rank != 0) {
               bar = peer_address(bar, 0);
@@ -461,9 +478,6 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
             } else {
               mbar_expect(bar, kStageBytes);
             }
-            const uint32_t a = ring + s * kStageBytes, b = a + 16384;
-            const bool a_mn = reads_mn<BN>(g, p.kind, true, i, kb);
-            const bool b_mn = reads_mn<BN>(g, p.kind, false, j, kb);
 #pragma unroll
             for (int q = 0; q < 2; ++q)
               tma_load<CG>(a + q * 8192, ma, bar, a_mn ? a0 + 64 * q : kb * 64,
@@ -473,8 +487,16 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
               tma_load<CG>(b + q * 8192, mb, bar, b_mn ? b0 + 64 * q : kb * 64,
                            b_mn ? kb * 64 : b0 + 64 * q, z);
           }
+          __syncwarp();
+          ++issued;
+          if (++s == S) {
+            s = 0;
+            turn ^= 1u;
+          }
         }
       }
+    }
+    if (elect_one()) {
       issued_s = issued;
       if (CG == 2 && rank != 0)
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
@@ -483,8 +505,8 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
                      : "memory");
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      uint32_t used = 0, n = 0;
+    if (rank == 0) {
+      uint32_t n = 0, s = 0, turn = 0;
       bool ok = true;
       for (int ph = 0; ok && ph < phases; ++ph) {
         const Phase p = phase_of<CG, BN>(g, ph);
@@ -492,18 +514,15 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
           int z, i, j;
           tile_of(g, p, t, z, i, j);
           const uint32_t acc = n & 1u;
-          if (!mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1u) ^ 1u, g.wait_ns, stop_v)) {
-            ok = false;
-            break;
-          }
+          ok = mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1u) ^ 1u, g.wait_ns, stop_v);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
           fence_after();
           const uint32_t d = tmem + acc * BN;
-          for (int kb = 0; kb < p.kblocks; ++kb, ++used) {
-            const int s = (int)(used % S);
-            if (!mbar_wait(smem_u32(&full[s]), (used / S) & 1u, g.wait_ns, stop_v)) {
-              ok = false;
-              break;
-            }
+          for (int kb = 0; kb < p.kblocks; ++kb) {
+            ok = mbar_wait(smem_u32(&full[s]), turn, g.wait_ns, stop_v);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
             fence_after();
             const uint32_t a = ring + s * kStageBytes, b = a + 16384;
             const bool a_mn = reads_mn<BN>(g, p.kind, true, i, kb);
@@ -511,23 +530,33 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
             const uint32_t idesc = instruction_desc<CG, BN>(a_mn, b_mn);
             const uint64_t da = operand_desc(a, a_mn), db = operand_desc(b, b_mn);
             const uint64_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16<CG>(d, da + k * sa, db + k * sb, idesc, (kb | k) != 0);
-            mma_commit<CG>(smem_u32(&empty[s]));
+              for (int k = 0; k < 4; ++k)
+                mma_f16<CG>(d, da + k * sa, db + k * sb, idesc, (kb | k) != 0);
+              mma_commit<CG>(smem_u32(&empty[s]));
+            }
+            __syncwarp();
+            if (++s == S) {
+              s = 0;
+              turn ^= 1u;
+            }
           }
-          if (ok) mma_commit<CG>(smem_u32(&acc_full[acc]));
+          if (ok && elect_one()) mma_commit<CG>(smem_u32(&acc_full[acc]));
+          __syncwarp();
         }
       }
       // The MMAs in flight end before TMEM and the operands go.
-      if constexpr (CG == 2)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                smem_u32(&drained))
-            : "memory");
-      else
-        mma_commit<1>(smem_u32(&drained));
-      mbar_drain(smem_u32(&drained), 0);
+      if (elect_one()) {
+        if constexpr (CG == 2)
+          asm volatile(
+              "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                  smem_u32(&drained))
+              : "memory");
+        else
+          mma_commit<1>(smem_u32(&drained));
+        mbar_drain(smem_u32(&drained), 0);
+      }
     }
   } else {
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
