@@ -26,7 +26,6 @@ constexpr int kMuonBlock = 128;          // values per quantization scale
 constexpr int kMuonMaxSteps = 16;
 constexpr int kMuonMaxParts = 256;       // partial sums of one matrix's norm
 constexpr int kMuonHdrStatus = 4;        // header word, as in the MicroAdam state
-constexpr int kMuonHdrBarrier = 5;       // of the workspace: arrivals at the grid barrier
 constexpr uint32_t kMuonNonFinite = 1u;
 constexpr uint32_t kMuonTimeout = 2u;
 
@@ -68,16 +67,16 @@ cudaError_t muon_launch_direction_norm(const MuonShape& s, const MuonQuant& q, c
                                        cudaStream_t st);
 // X_0 in fp16: x 2^(e0 - t) with 2^(t-1) <= |x|_F + eps < 2^t, an exact scaling;
 // factor[i] = 2^t / (|x|_F + eps) is applied in fp32 by the first products.
-// Both also zero the grid barrier's count.
+// Both also zero the matrices' counters.
 cudaError_t muon_launch_load(const MuonShape& s, const MuonView& x, const double* partials,
-                             float eps, int e0, void* X, float* factor, uint32_t* barrier,
+                             float eps, int e0, void* X, float* factor, uint32_t* counters,
                              cudaStream_t st);
 // The momentum update; direction U to `out` (fp32 or bf16, contiguous), or,
 // with X != NULL, straight to X_0 as in muon_launch_load.
 cudaError_t muon_launch_momentum(const MuonShape& s, const MuonQuant& q, const void* g, int g_type,
                                  float beta, int nesterov, const MuonRandom& rnd, void* out,
                                  int out_type, const double* partials, float eps, int e0, void* X,
-                                 float* factor, uint32_t* barrier, cudaStream_t st);
+                                 float* factor, uint32_t* counters, cudaStream_t st);
 cudaError_t muon_launch_read(const MuonShape& s, const MuonQuant& q, void* out, int out_type,
                              cudaStream_t st);
 cudaError_t muon_launch_write(const MuonShape& s, const MuonQuant& q, const void* values, int type,
@@ -103,7 +102,7 @@ struct MuonNs {
   int64_t ldo, batch_stride;   // in elements
   int32_t params, out_type, out_vec;
   float decay;
-  uint32_t* barrier;           // arrivals at the grid barrier, 0 at the launch
+  uint32_t* counters;          // per matrix: finished parts of tiles, 0 at the launch
   uint32_t* status;
   uint64_t wait_ns;            // longest wait inside the kernel before it gives up
 };

@@ -27,7 +27,7 @@ struct mua_muon_ctx {
   int32_t group, parts;
   int64_t bpm;               // blocks of one matrix
   int64_t off_scales, off_codes, state_bytes;
-  int64_t off_partials, off_factor, off_x[2], off_a, off_p, workspace_bytes;
+  int64_t off_partials, off_factor, off_counters, off_x[2], off_a, off_p, workspace_bytes;
   float coef[mua::kMuonMaxSteps][3];
   int32_t ex[mua::kMuonMaxSteps + 1], ea[mua::kMuonMaxSteps], ep[mua::kMuonMaxSteps];
   int64_t wait_ns;
@@ -126,8 +126,8 @@ struct Target {  // where the last product goes
   float decay;
 };
 
-uint32_t* barrier_word(uint8_t* ws) {
-  return reinterpret_cast<uint32_t*>(ws) + mua::kMuonHdrBarrier;
+uint32_t* counters(const mua_muon_ctx* h, uint8_t* ws) {
+  return reinterpret_cast<uint32_t*>(ws + h->off_counters);
 }
 
 // The Newton-Schulz steps of matrices first .. first + count - 1, X_0 and its
@@ -168,7 +168,7 @@ int iterate(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count, co
   g.out_vec = aligned(g.out, 4 * size) && to.row_stride % 4 == 0 &&
               (count == 1 || to.matrix_stride % 4 == 0);
   g.decay = to.decay;
-  g.barrier = barrier_word(ws);
+  g.counters = counters(h, ws);
   g.status = status;
   g.wait_ns = (uint64_t)std::max<int64_t>(0, h->wait_ns);
   const cudaError_t e = mua::muon_launch_ns(m, g, st);
@@ -232,6 +232,7 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
   };
   h->off_partials = take((int64_t)h->group * h->parts * 8);
   h->off_factor = take((int64_t)h->group * 4);
+  h->off_counters = take((int64_t)h->group * 4);
   h->off_x[0] = take(h->group * x_bytes);
   h->off_x[1] = steps > 1 ? take(h->group * x_bytes) : h->off_x[0];
   h->off_a = take(h->group * a_bytes);
@@ -342,7 +343,7 @@ int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t 
     cudaError_t e = mua::muon_launch_norm(shape(h, count), v, partials, st);
     if (e != cudaSuccess) return fail(e, "norm kernel launch");
     e = mua::muon_launch_load(shape(h, count), v, partials, eps, h->ex[0], ws + h->off_x[0],
-                              reinterpret_cast<float*>(ws + h->off_factor), barrier_word(ws), st);
+                              reinterpret_cast<float*>(ws + h->off_factor), counters(h, ws), st);
     if (e != cudaSuccess) return fail(e, "load kernel launch");
     const int rc = iterate(h, ws, first, count, to,
                            reinterpret_cast<uint32_t*>(ws) + mua::kMuonHdrStatus, st);
@@ -380,7 +381,7 @@ int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* g
     if (e != cudaSuccess) return fail(e, "direction norm kernel launch");
     e = mua::muon_launch_momentum(s, q, g, grads_type, beta, nesterov != 0,
                                   random_keys(h, first, t, seed), nullptr, 0, partials, eps,
-                                  h->ex[0], ws + h->off_x[0], factor, barrier_word(ws), st);
+                                  h->ex[0], ws + h->off_x[0], factor, counters(h, ws), st);
     if (e != cudaSuccess) return fail(e, "momentum kernel launch");
     const int rc = iterate(h, ws, first, count, to,
                            static_cast<uint32_t*>(state) + mua::kMuonHdrStatus, st);

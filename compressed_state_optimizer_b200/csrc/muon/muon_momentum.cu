@@ -248,7 +248,7 @@ template <int BITS, int G, int OUT>
 __global__ void __launch_bounds__(kThreads)
 momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nesterov,
                 const __grid_constant__ MuonRandom rnd, void* out, const double* partials,
-                float eps, int e0, void* X, float* factor, uint32_t* barrier, int splits) {
+                float eps, int e0, void* X, float* factor, uint32_t* counters, int splits) {
   wait_previous();
   release_next();
   const int mat = blockIdx.x / splits, split = blockIdx.x - mat * splits;
@@ -277,8 +277,10 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
   NormScale ns;
   if constexpr (OUT == 2) {
     ns = norm_scale(partials + (int64_t)mat * s.parts, s.parts, eps, e0);
-    if (split == 0 && threadIdx.x == 0) factor[mat] = ns.factor;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *barrier = 0;
+    if (split == 0 && threadIdx.x == 0) {
+      factor[mat] = ns.factor;
+      counters[mat] = 0;
+    }
   }
   bool bad = false;
 #pragma unroll
@@ -403,7 +405,7 @@ norm_kernel(MuonShape s, MuonView x, double* partials) {
 template <int T>
 __global__ void __launch_bounds__(kThreads)
 load_kernel(MuonShape s, MuonView x, const double* partials, float eps, int e0, void* X,
-            float* factor, uint32_t* barrier, int splits) {
+            float* factor, uint32_t* counters, int splits) {
   wait_previous();
   release_next();
   const int mat = blockIdx.x / splits, split = blockIdx.x - mat * splits;
@@ -412,8 +414,10 @@ load_kernel(MuonShape s, MuonView x, const double* partials, float eps, int e0, 
   const bool vec = aligned16(xm) && (x.row_stride * es) % 16 == 0;
   const uint32_t per_row = (uint32_t)(s.ld / 8), groups = per_row * (uint32_t)s.rows;
   const NormScale ns = norm_scale(partials + (int64_t)mat * s.parts, s.parts, eps, e0);
-  if (split == 0 && threadIdx.x == 0) factor[mat] = ns.factor;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *barrier = 0;
+  if (split == 0 && threadIdx.x == 0) {
+    factor[mat] = ns.factor;
+    counters[mat] = 0;
+  }
   __half* out = static_cast<__half*>(X) + (int64_t)mat * s.rows * s.ld;
   for (uint64_t q = (uint64_t)split * kThreads + threadIdx.x; q < groups;
        q += (uint64_t)splits * kThreads) {
@@ -525,14 +529,14 @@ cudaError_t muon_launch_norm(const MuonShape& s, const MuonView& x, double* part
 }
 
 cudaError_t muon_launch_load(const MuonShape& s, const MuonView& x, const double* partials,
-                             float eps, int e0, void* X, float* factor, uint32_t* barrier,
+                             float eps, int e0, void* X, float* factor, uint32_t* counters,
                              cudaStream_t st) {
   // Two 16-byte groups per thread.
   const int64_t groups = (int64_t)s.rows * (s.ld / 8);
   const int splits = (int)((groups + 2 * kThreads - 1) / (2 * kThreads));
   const int64_t grid = (int64_t)s.count * splits;
   auto k = x.type == kBf16 ? load_kernel<kBf16> : load_kernel<kF32>;
-  return launch(k, grid, st, true, s, x, partials, eps, e0, X, factor, barrier, splits);
+  return launch(k, grid, st, true, s, x, partials, eps, e0, X, factor, counters, splits);
 }
 
 cudaError_t muon_launch_direction_norm(const MuonShape& s, const MuonQuant& q, const void* g,
@@ -556,13 +560,13 @@ static auto pick_momentum(int bits, int g_type) {
 cudaError_t muon_launch_momentum(const MuonShape& s, const MuonQuant& q, const void* g, int g_type,
                                  float beta, int nesterov, const MuonRandom& rnd, void* out,
                                  int out_type, const double* partials, float eps, int e0, void* X,
-                                 float* factor, uint32_t* barrier, cudaStream_t st) {
+                                 float* factor, uint32_t* counters, cudaStream_t st) {
   const int64_t splits = chunk_splits(q);
   auto k = X ? pick_momentum<2>(q.bits, g_type)
              : (out_type == kBf16 ? pick_momentum<1>(q.bits, g_type)
                                   : pick_momentum<0>(q.bits, g_type));
   return launch(k, splits * s.count, st, X != nullptr, s, q, g, beta, nesterov, rnd, out, partials,
-                eps, e0, X, factor, barrier, (int)splits);
+                eps, e0, X, factor, counters, (int)splits);
 }
 
 cudaError_t muon_launch_read(const MuonShape& s, const MuonQuant& q, void* out, int out_type,

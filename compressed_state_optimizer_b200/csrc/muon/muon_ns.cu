@@ -1,7 +1,8 @@
 // The Newton-Schulz iteration of a stack of matrices in one launch, on the
 // tensor cores (tcgen05.mma, fp16 operands, fp32 accumulators in TMEM).
 //
-// Three products per step, each with its epilogue fused, a grid barrier between:
+// Three products per step, each with its epilogue fused, every matrix of the
+// stack at its own pace (a product starts when the one before it is complete):
 //   A  = f^2 X X^T          symmetric: lower block triangle only
 //   P  = a I + b A + c A A  likewise, the polynomial formed in the epilogue
 //   X' = f P X              (X P for a tall matrix); the last one writes the
@@ -16,7 +17,7 @@
 // both operands, 8 KB of shared memory read per 16-deep MMA and SM instead of
 // 12) or 128 x 128 on one CTA when the 256-wide tiles would be too few for the
 // SMs. Per CTA: warp 0 streams 64-deep operand slices into a ring of 128-byte
-// swizzled shared tiles (TMA), warp 1 issues the MMAs, warps 2..5 turn
+// swizzled shared tiles (TMA), warp 1 issues the MMAs, warps 2..9 turn
 // finished accumulators into output while the next tile's MMAs run into the
 // other half of TMEM.
 //
@@ -33,12 +34,17 @@
 namespace mua {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kEpilogueWarps = 4;
-constexpr int kStages = 6;
+constexpr int kEpilogueWarps = 8;            // two for each quarter of the TMEM lanes
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kStageBytes = 32768;           // 128 rows of A and of B, 64 deep
 constexpr int kChunkBytes = 4096;            // 32 rows x 64 fp16 columns of output
-constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * 2 * kChunkBytes + 1024;
+template <int BN>
+struct Ring {
+  static constexpr int chunks = BN / 128;    // an epilogue warp's share of a tile
+  static constexpr int stages = BN == 256 ? 5 : 6;
+  static constexpr int smem =
+      stages * kStageBytes + kEpilogueWarps * chunks * kChunkBytes + 1024;  // + alignment
+};
 constexpr uint64_t kDrainNs = 2000000000ull;  // bound on waits for copies and MMAs in flight
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -247,50 +253,67 @@ struct Maps {
 
 enum Product : int { kGram = 0, kPoly = 1, kUpdate = 2 };
 
-// One product of the iteration: output tiles and contraction length.
-struct Phase {
-  int step, kind, tm, tn, kblocks;
-  int64_t tiles;  // of the whole stack
+// Tiles of one matrix in a symmetric product (the lower block triangle) and in
+// an update.
+struct Tiles {
+  int sm, um, un;      // blocks of the short side; row and column tiles of X
+  int gram, update;    // k-slices of the products (gram: along the long side)
+  int sym, upd;        // tiles
 };
-template <int CG, int BN>
-__device__ __forceinline__ Phase phase_of(const MuonNs& g, int ph) {
-  Phase p;
-  p.step = ph / 3;
-  p.kind = ph - 3 * p.step;
+template <int BN>
+__device__ __forceinline__ Tiles tiles_of(const MuonNs& g) {
   const int s = min(g.rows, g.cols), l = max(g.rows, g.cols);
-  if (p.kind == kUpdate) {
-    p.tm = (g.rows + CG * 128 - 1) / (CG * 128);
-    p.tn = (g.cols + BN - 1) / BN;
-    p.tiles = (int64_t)p.tm * p.tn * g.batch;
-  } else {
-    p.tm = p.tn = (s + BN - 1) / BN;
-    p.tiles = (int64_t)p.tm * (p.tm + 1) / 2 * g.batch;
-  }
-  p.kblocks = ((p.kind == kGram ? l : s) + 63) / 64;
-  return p;
+  Tiles t;
+  t.sm = (s + BN - 1) / BN;
+  t.um = (g.rows + BN - 1) / BN;
+  t.un = (g.cols + BN - 1) / BN;
+  t.gram = (l + 63) / 64;
+  t.update = (s + 63) / 64;
+  t.sym = t.sm * (t.sm + 1) / 2;
+  t.upd = t.um * t.un;
+  return t;
 }
-// Tile t: matrix, row tile, column tile. The triangle is walked row by row;
-// the update walks the short side's tiles first, so that tiles in flight share
-// their slice of X.
-__device__ __forceinline__ void tile_of(const MuonNs& g, const Phase& p, int64_t t, int& z, int& i,
-                                        int& j) {
-  const int per = p.kind == kUpdate ? p.tm * p.tn : p.tm * (p.tm + 1) / 2;
-  z = (int)(t / per);
-  const int r = (int)(t - (int64_t)z * per);
-  if (p.kind == kUpdate) {
+
+// Work item w of the launch, in the order (step, product, matrix, tile): tile
+// (i, j) of a product of matrix z, which needs `before` finished tiles of z.
+// The triangle is walked row by row; the update walks the short side's tiles
+// first, so that tiles in flight share their slice of X.
+struct Item {
+  int step, kind, z, i, j, kblocks;
+  uint32_t before;
+  bool last;
+};
+__device__ __forceinline__ int64_t item_count(const MuonNs& g, const Tiles& T) {
+  return (int64_t)(2 * T.sym + T.upd) * g.batch * g.steps;
+}
+__device__ __forceinline__ Item item_of(const MuonNs& g, const Tiles& T, int64_t w) {
+  Item it;
+  const int64_t sym = (int64_t)T.sym * g.batch, per = 2 * sym + (int64_t)T.upd * g.batch;
+  it.step = (int)(w / per);
+  int64_t r = w - it.step * per;
+  it.kind = r < sym ? kGram : (r < 2 * sym ? kPoly : kUpdate);
+  r -= it.kind * sym;
+  const int tiles = it.kind == kUpdate ? T.upd : T.sym;
+  it.z = (int)(r / tiles);
+  const int t = (int)(r - (int64_t)it.z * tiles);
+  it.before = (uint32_t)(it.step * (2 * T.sym + T.upd) + it.kind * T.sym);
+  it.kblocks = it.kind == kGram ? T.gram : T.update;
+  it.last = it.kind == kUpdate && it.step == g.steps - 1;
+  if (it.kind == kUpdate) {
     if (g.rows <= g.cols) {
-      j = r / p.tm;
-      i = r - j * p.tm;
+      it.j = t / T.um;
+      it.i = t - it.j * T.um;
     } else {
-      i = r / p.tn;
-      j = r - i * p.tn;
+      it.i = t / T.un;
+      it.j = t - it.i * T.un;
     }
   } else {
-    i = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
-    while (i * (i + 1) / 2 > r) --i;
-    while ((i + 1) * (i + 2) / 2 <= r) ++i;
-    j = r - i * (i + 1) / 2;
+    it.i = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while (it.i * (it.i + 1) / 2 > t) --it.i;
+    while ((it.i + 1) * (it.i + 2) / 2 <= t) ++it.i;
+    it.j = t - it.i * (it.i + 1) / 2;
   }
+  return it;
 }
 // Whether slice kb of the operand with M / N block `block` is read with its
 // M / N index contiguous. X has one major per product; A and P (symmetric)
@@ -373,13 +396,18 @@ __device__ __forceinline__ void write_out(const MuonNs& g, int64_t at, int left,
   }
 }
 
-// Waits until every CTA has finished the phases before `ph`.
-__device__ __forceinline__ bool grid_wait(const MuonNs& g, int ph, volatile uint32_t* stop) {
-  const uint32_t want = gridDim.x * (uint32_t)ph;
+// Waits until matrix z has `tiles` finished tiles (every epilogue warp of a
+// tile counts one). Items are taken in order by CTAs that are all resident, and
+// need earlier items only, so the wait ends.
+__device__ __forceinline__ bool matrix_wait(const MuonNs& g, int z, uint32_t want,
+                                            volatile uint32_t* stop) {
+  const uint32_t* p = g.counters + z;
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  if (v >= want) return true;
   const uint64_t t0 = now_ns();
   while (true) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(g.barrier) : "memory");
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     if (v >= want) return true;
     if (*stop) return false;
     if (g.wait_ns == 0 || now_ns() - t0 > g.wait_ns) {
@@ -392,17 +420,19 @@ __device__ __forceinline__ bool grid_wait(const MuonNs& g, int ph, volatile uint
 template <int CG, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
 ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
-  constexpr int S = kStages;
+  constexpr int S = Ring<BN>::stages;
+  constexpr int kChunks = Ring<BN>::chunks;
   constexpr uint32_t kTmemCols = 2 * BN;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drained;
-  __shared__ __align__(8) uint64_t addend_full[kEpilogueWarps][2];
-  __shared__ uint32_t tmem_base_s, stop, issued_s, peer_issued_s, epilogue_go;
+  __shared__ __align__(8) uint64_t addend_full[kEpilogueWarps][kChunks];
+  __shared__ uint32_t tmem_base_s, stop, issued_s, peer_issued_s;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? (blockIdx.x & 1u) : 0u;
   const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
-  const int phases = 3 * g.steps;
+  const Tiles tiles = tiles_of<BN>(g);
+  const int64_t items = item_count(g, tiles);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -412,8 +442,9 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&acc_full[a]), 1);
       mbar_init(smem_u32(&acc_empty[a]), kEpilogueWarps * CG);
-      for (int w = 0; w < kEpilogueWarps; ++w) mbar_init(smem_u32(&addend_full[w][a]), 1);
     }
+    for (int w = 0; w < kEpilogueWarps; ++w)
+      for (int c = 0; c < kChunks; ++c) mbar_init(smem_u32(&addend_full[w][c]), 1);
     mbar_init(smem_u32(&drained), 1);
     stop = 0;
     issued_s = peer_issued_s = 0;
@@ -445,54 +476,55 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
   if (warp == 0) {
     uint32_t issued = 0, s = 0, turn = 1;
     bool ok = true;
-    for (int ph = 0; ok && ph < phases; ++ph) {
-      if (ph > 0) {
-        ok = grid_wait(g, ph, stop_v);
+    int ready_z = -1;
+    uint32_t ready = 0;
+    for (int64_t w = first; ok && w < items; w += stride) {
+      const Item it = item_of(g, tiles, w);
+      if (it.z != ready_z || it.before != ready) {
+        ok = matrix_wait(g, it.z, it.before * (CG * kEpilogueWarps), stop_v);
         ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        fence_async_global();
+        ready_z = it.z;
+        ready = it.before;
       }
-      fence_async_global();
-      const Phase p = phase_of<CG, BN>(g, ph);
-      const CUtensorMap* x = &maps.load_x[p.step & 1];
       const bool tall = g.rows > g.cols;
-      const CUtensorMap* ma = p.kind == kGram ? x : (p.kind == kPoly ? &maps.load_a
-                                                                     : (tall ? x : &maps.load_p));
-      const CUtensorMap* mb = p.kind == kGram ? x : (p.kind == kPoly ? &maps.load_a
-                                                                     : (tall ? &maps.load_p : x));
-      for (int64_t t = first; ok && t < p.tiles; t += stride) {
-        int z, i, j;
-        tile_of(g, p, t, z, i, j);
-        const int a0 = i * CG * 128 + (int)rank * 128;  // this CTA's rows of A
-        const int b0 = j * BN + (int)rank * (BN / CG);  // and of B
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          ok = mbar_wait(smem_u32(&empty[s]), turn, g.wait_ns, stop_v);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          const uint32_t a = ring + s * kStageBytes, b = a + 16384;
-          const bool a_mn = reads_mn<BN>(g, p.kind, true, i, kb);
-          const bool b_mn = reads_mn<BN>(g, p.kind, false, j, kb);
-          if (elect_one()) {
-            uint32_t bar = smem_u32(&full[s]);
-            if (CG == 2 && rank != 0) {
-              bar = peer_address(bar, 0);
-              mbar_expect_cluster(bar, kStageBytes);
-            } else {
-              mbar_expect(bar, kStageBytes);
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-              tma_load<CG>(a + q * 8192, ma, bar, a_mn ? a0 + 64 * q : kb * 64,
-                           a_mn ? kb * 64 : a0 + 64 * q, z);
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-              tma_load<CG>(b + q * 8192, mb, bar, b_mn ? b0 + 64 * q : kb * 64,
-                           b_mn ? kb * 64 : b0 + 64 * q, z);
+      const CUtensorMap* x = &maps.load_x[it.step & 1];
+      const CUtensorMap* ma = it.kind == kGram ? x : (it.kind == kPoly ? &maps.load_a
+                                                                       : (tall ? x : &maps.load_p));
+      const CUtensorMap* mb = it.kind == kGram ? x : (it.kind == kPoly ? &maps.load_a
+                                                                       : (tall ? &maps.load_p : x));
+      const int a0 = it.i * BN + (int)rank * 128;         // this CTA's rows of A
+      const int b0 = it.j * BN + (int)rank * (BN / CG);   // and of B
+      for (int kb = 0; kb < it.kblocks; ++kb) {
+        ok = mbar_wait(smem_u32(&empty[s]), turn, g.wait_ns, stop_v);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        const uint32_t a = ring + s * kStageBytes, b = a + 16384;
+        const bool a_mn = reads_mn<BN>(g, it.kind, true, it.i, kb);
+        const bool b_mn = reads_mn<BN>(g, it.kind, false, it.j, kb);
+        if (elect_one()) {
+          uint32_t bar = smem_u32(&full[s]);
+          if (CG == 2 && rank != 0) {
+            bar = peer_address(bar, 0);
+            mbar_expect_cluster(bar, kStageBytes);
+          } else {
+            mbar_expect(bar, kStageBytes);
           }
-          __syncwarp();
-          ++issued;
-          if (++s == S) {
-            s = 0;
-            turn ^= 1u;
-          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            tma_load<CG>(a + q * 8192, ma, bar, a_mn ? a0 + 64 * q : kb * 64,
+                         a_mn ? kb * 64 : a0 + 64 * q, it.z);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            tma_load<CG>(b + q * 8192, mb, bar, b_mn ? b0 + 64 * q : kb * 64,
+                         b_mn ? kb * 64 : b0 + 64 * q, it.z);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == S) {
+          s = 0;
+          turn ^= 1u;
         }
       }
     }
@@ -508,43 +540,39 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
     if (rank == 0) {
       uint32_t n = 0, s = 0, turn = 0;
       bool ok = true;
-      for (int ph = 0; ok && ph < phases; ++ph) {
-        const Phase p = phase_of<CG, BN>(g, ph);
-        for (int64_t t = first; ok && t < p.tiles; t += stride, ++n) {
-          int z, i, j;
-          tile_of(g, p, t, z, i, j);
-          const uint32_t acc = n & 1u;
-          ok = mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1u) ^ 1u, g.wait_ns, stop_v);
+      for (int64_t w = first; ok && w < items; w += stride, ++n) {
+        const Item it = item_of(g, tiles, w);
+        const uint32_t acc = n & 1u;
+        ok = mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1u) ^ 1u, g.wait_ns, stop_v);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        fence_after();
+        const uint32_t d = tmem + acc * BN;
+        for (int kb = 0; kb < it.kblocks; ++kb) {
+          ok = mbar_wait(smem_u32(&full[s]), turn, g.wait_ns, stop_v);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           fence_after();
-          const uint32_t d = tmem + acc * BN;
-          for (int kb = 0; kb < p.kblocks; ++kb) {
-            ok = mbar_wait(smem_u32(&full[s]), turn, g.wait_ns, stop_v);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            fence_after();
-            const uint32_t a = ring + s * kStageBytes, b = a + 16384;
-            const bool a_mn = reads_mn<BN>(g, p.kind, true, i, kb);
-            const bool b_mn = reads_mn<BN>(g, p.kind, false, j, kb);
-            const uint32_t idesc = instruction_desc<CG, BN>(a_mn, b_mn);
-            const uint64_t da = operand_desc(a, a_mn), db = operand_desc(b, b_mn);
-            const uint64_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
-            if (elect_one()) {
+          const uint32_t a = ring + s * kStageBytes, b = a + 16384;
+          const bool a_mn = reads_mn<BN>(g, it.kind, true, it.i, kb);
+          const bool b_mn = reads_mn<BN>(g, it.kind, false, it.j, kb);
+          const uint32_t idesc = instruction_desc<CG, BN>(a_mn, b_mn);
+          const uint64_t da = operand_desc(a, a_mn), db = operand_desc(b, b_mn);
+          const uint64_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+          if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f16<CG>(d, da + k * sa, db + k * sb, idesc, (kb | k) != 0);
-              mma_commit<CG>(smem_u32(&empty[s]));
-            }
-            __syncwarp();
-            if (++s == S) {
-              s = 0;
-              turn ^= 1u;
-            }
+            for (int k = 0; k < 4; ++k)
+              mma_f16<CG>(d, da + k * sa, db + k * sb, idesc, (kb | k) != 0);
+            mma_commit<CG>(smem_u32(&empty[s]));
           }
-          if (ok && elect_one()) mma_commit<CG>(smem_u32(&acc_full[acc]));
           __syncwarp();
+          if (++s == S) {
+            s = 0;
+            turn ^= 1u;
+          }
         }
+        if (ok && elect_one()) mma_commit<CG>(smem_u32(&acc_full[acc]));
+        __syncwarp();
       }
       // The MMAs in flight end before TMEM and the operands go.
       if (elect_one()) {
@@ -559,171 +587,147 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
       }
     }
   } else {
-    const int quarter = warp & 3;  // the TMEM lanes this warp may read
-    const uint32_t stage = ring + S * kStageBytes + (warp - 2) * 2 * kChunkBytes;
-    uint32_t n = 0, chunk = 0;       // tiles, staged chunks
-    uint32_t asked = 0, parity = 0;  // per buffer: an addend copy in flight, its barrier's phase
+    const int quarter = warp & 3;     // the TMEM lanes this warp may read
+    const int side = (warp - 2) >> 2;  // its half of the tile's columns
+    const uint32_t stage = ring + S * kStageBytes + (warp - 2) * kChunks * kChunkBytes;
+    uint32_t n = 0;
+    uint32_t asked = 0, parity = 0;  // per chunk: an addend copy in flight, its barrier's phase
+    int ready_z = -1;
+    uint32_t ready = 0;
     bool ok = true;
-    for (int ph = 0; ok && ph < phases; ++ph) {
-      const Phase p = phase_of<CG, BN>(g, ph);
-      const bool last = ph == phases - 1;
-      const int M = p.kind == kUpdate ? g.rows : min(g.rows, g.cols);
-      const int N = p.kind == kUpdate ? g.cols : M;
-      const CUtensorMap* out = p.kind == kGram ? &maps.store_a
-                                               : (p.kind == kPoly ? &maps.store_p
-                                                                  : &maps.store_x[(p.step & 1) ^ 1]);
-      if (p.kind == kPoly && first < p.tiles) {
-        if (lane == 0) ok = grid_wait(g, ph, stop_v);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        fence_async_global();
-      }
-      for (int64_t t = first; ok && t < p.tiles; t += stride, ++n) {
-        int z, i, j;
-        tile_of(g, p, t, z, i, j);
-        const int row0 = i * CG * 128 + (int)rank * 128 + quarter * 32;
-        const int chunks = row0 < M ? (min(BN, N - j * BN) + 63) / 64 : 0;
-        const uint32_t acc = n & 1u;
-        // The addend's first chunk on its way while the MMAs run.
-        if (p.kind == kPoly && chunks > 0) {
-          if (lane == 0) {
-            tma_store_read_wait<0>();
-            const uint32_t bar = smem_u32(&addend_full[warp - 2][chunk & 1u]);
-            mbar_expect(bar, kChunkBytes);
-            tma_load<1>(stage + (chunk & 1u) * kChunkBytes, &maps.store_a, bar, j * BN, row0, z);
-          }
-          asked |= 1u << (chunk & 1u);
+    for (int64_t w = first; ok && w < items; w += stride, ++n) {
+      const Item it = item_of(g, tiles, w);
+      const int M = it.kind == kUpdate ? g.rows : min(g.rows, g.cols);
+      const int N = it.kind == kUpdate ? g.cols : M;
+      const int row0 = it.i * BN + (int)rank * 128 + quarter * 32;
+      const int col0 = it.j * BN + side * (BN / 2);
+      const int chunks = row0 < M ? max(0, min(kChunks, (N - col0 + 63) / 64)) : 0;
+      const uint32_t acc = n & 1u;
+      if (it.kind == kPoly && chunks > 0) {
+        // The addend on its way while the MMAs run.
+        if (it.z != ready_z || it.before != ready) {
+          ok = matrix_wait(g, it.z, it.before * (CG * kEpilogueWarps), stop_v);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          fence_async_global();
+          ready_z = it.z;
+          ready = it.before;
         }
-        ok = mbar_wait(smem_u32(&acc_full[acc]), (n >> 1) & 1u, g.wait_ns, stop_v);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN;
-        if (ok) {
-          fence_after();
-          float f = g.factor && p.step == 0 && p.kind != kPoly ? g.factor[z] : 1.0f;
-          if (p.kind == kGram) f *= f;
-          const float alpha = f * (p.kind == kGram ? g.gram_alpha[p.step]
-                                                   : (p.kind == kPoly ? g.poly_alpha[p.step]
-                                                                      : g.update_alpha[p.step]));
-          if (!last) {
-            const float mid = g.poly_mid[p.step], diag = g.poly_diag[p.step];
-#pragma unroll 1
-            for (int c = 0; c < chunks; ++c, ++chunk) {
-              const uint32_t tile = stage + (chunk & 1u) * kChunkBytes;
-              uint32_t v[2][32];
-              tmem_load32(lanes + 64 * c, v[0]);
-              tmem_load32(lanes + 64 * c + 32, v[1]);
-              // This buffer's last store has been read; the other's too before the
-              // next addend lands there.
-              if (p.kind == kPoly) {
-                if (c + 1 < chunks) {
-                  const uint32_t next = (chunk + 1) & 1u;
-                  if (lane == 0) {
-                    tma_store_read_wait<0>();
-                    const uint32_t bar = smem_u32(&addend_full[warp - 2][next]);
-                    mbar_expect(bar, kChunkBytes);
-                    tma_load<1>(stage + next * kChunkBytes, &maps.store_a, bar,
-                                j * BN + 64 * (c + 1), row0, z);
-                  }
-                  asked |= 1u << next;
-                }
-                const uint32_t now = chunk & 1u;
-                mbar_drain(smem_u32(&addend_full[warp - 2][now]), (parity >> now) & 1u);
-                asked &= ~(1u << now);
-                parity ^= 1u << now;
-              } else {
-                if (lane == 0) tma_store_read_wait<1>();
-              }
-              __syncwarp();
-              tmem_load_wait();
-              const int diagonal = row0 + lane - (j * BN + 64 * c);  // column of the diagonal
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const uint32_t at = chunk_address(tile, lane, q);
-                uint32_t w[4];
-                if (p.kind == kPoly) {
-                  const uint4 a = ld_shared(at);
-                  const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const __half2 h = *reinterpret_cast<const __half2*>(&aw[e]);
-                    float x0 = __uint_as_float(v[q >> 2][(8 * q + 2 * e) & 31]) * alpha;
-                    float x1 = __uint_as_float(v[q >> 2][(8 * q + 2 * e + 1) & 31]) * alpha;
-                    x0 = fmaf(__low2float(h), mid, x0);
-                    x1 = fmaf(__high2float(h), mid, x1);
-                    if (8 * q + 2 * e == diagonal) x0 += diag;
-                    if (8 * q + 2 * e + 1 == diagonal) x1 += diag;
-                    w[e] = pack_f16(x0, x1);
-                  }
-                } else {
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    w[e] = pack_f16(__uint_as_float(v[q >> 2][(8 * q + 2 * e) & 31]) * alpha,
-                                    __uint_as_float(v[q >> 2][(8 * q + 2 * e + 1) & 31]) * alpha);
-                }
-                st_shared(at, w[0], w[1], w[2], w[3]);
-              }
-              fence_async_shared();
-              __syncwarp();
-              if (lane == 0) tma_store(out, tile, j * BN + 64 * c, row0, z);
-            }
-          } else {
-            if (lane == 0) tma_store_read_wait<0>();
-            __syncwarp();
-            // 32 x 32 fp32 through shared memory: a lane then holds four columns,
-            // eight lanes a row's 128 (64) contiguous bytes.
-#pragma unroll 1
-            for (int c = 0; c < 2 * chunks; ++c) {
-              uint32_t v[32];
-              tmem_load32(lanes + 32 * c, v);
-              tmem_load_wait();
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                st_shared(chunk_address(stage, lane, q), v[4 * q], v[4 * q + 1], v[4 * q + 2],
-                          v[4 * q + 3]);
-              __syncwarp();
-              const int col = j * BN + 32 * c + 4 * (lane & 7);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const int r = 4 * q + (lane >> 3), row = row0 + r;
-                const uint4 u = ld_shared(chunk_address(stage, r, lane & 7));
-                const float x[4] = {__uint_as_float(u.x), __uint_as_float(u.y),
-                                    __uint_as_float(u.z), __uint_as_float(u.w)};
-                if (row < M && col < N)
-                  write_out(g, (int64_t)z * g.batch_stride + (int64_t)row * g.ldo + col, N - col, x,
-                            alpha);
-              }
-              __syncwarp();
-            }
-          }
-        }
-        fence_before();
-        __syncwarp();
-        if (!ok) break;
         if (lane == 0) {
-          if (CG == 2 && rank != 0)
-            mbar_arrive_cluster(peer_address(smem_u32(&acc_empty[acc]), 0));
-          else
-            mbar_arrive(smem_u32(&acc_empty[acc]));
+          for (int c = 0; c < chunks; ++c) {
+            const uint32_t bar = smem_u32(&addend_full[warp - 2][c]);
+            mbar_expect(bar, kChunkBytes);
+            tma_load<1>(stage + c * kChunkBytes, &maps.store_a, bar, col0 + 64 * c, row0, it.z);
+          }
+        }
+        asked = (1u << chunks) - 1u;
+      }
+      ok = mbar_wait(smem_u32(&acc_full[acc]), (n >> 1) & 1u, g.wait_ns, stop_v);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      fence_after();
+      const uint32_t lanes =
+          tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + side * (BN / 2);
+      float f = it.step == 0 && it.kind != kPoly ? g.factor[it.z] : 1.0f;
+      if (it.kind == kGram) f *= f;
+      const float alpha = f * (it.kind == kGram ? g.gram_alpha[it.step]
+                                                : (it.kind == kPoly ? g.poly_alpha[it.step]
+                                                                    : g.update_alpha[it.step]));
+      if (!it.last) {
+        const float mid = g.poly_mid[it.step], diag = g.poly_diag[it.step];
+        const CUtensorMap* out = it.kind == kGram
+                                     ? &maps.store_a
+                                     : (it.kind == kPoly ? &maps.store_p
+                                                         : &maps.store_x[(it.step & 1) ^ 1]);
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          const uint32_t tile = stage + c * kChunkBytes;
+          uint32_t v[2][32];
+          tmem_load32(lanes + 64 * c, v[0]);
+          tmem_load32(lanes + 64 * c + 32, v[1]);
+          if (it.kind == kPoly) {
+            mbar_drain(smem_u32(&addend_full[warp - 2][c]), (parity >> c) & 1u);
+            asked &= ~(1u << c);
+            parity ^= 1u << c;
+          }
+          tmem_load_wait();
+          const int diagonal = row0 + lane - (col0 + 64 * c);  // column of the diagonal
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t at = chunk_address(tile, lane, q);
+            uint32_t h[4];
+            if (it.kind == kPoly) {
+              const uint4 a = ld_shared(at);
+              const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
+                float x0 = __uint_as_float(v[q >> 2][(8 * q + 2 * e) & 31]) * alpha;
+                float x1 = __uint_as_float(v[q >> 2][(8 * q + 2 * e + 1) & 31]) * alpha;
+                x0 = fmaf(y.x, mid, x0);
+                x1 = fmaf(y.y, mid, x1);
+                if (8 * q + 2 * e == diagonal) x0 += diag;
+                if (8 * q + 2 * e + 1 == diagonal) x1 += diag;
+                h[e] = pack_f16(x0, x1);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                h[e] = pack_f16(__uint_as_float(v[q >> 2][(8 * q + 2 * e) & 31]) * alpha,
+                                __uint_as_float(v[q >> 2][(8 * q + 2 * e + 1) & 31]) * alpha);
+            }
+            st_shared(at, h[0], h[1], h[2], h[3]);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) tma_store(out, tile, col0 + 64 * c, row0, it.z);
+        }
+      } else {
+        // 32 x 32 fp32 through shared memory: a lane then holds four columns,
+        // eight lanes a row's 128 (64) contiguous bytes.
+#pragma unroll 1
+        for (int c = 0; c < 2 * chunks; ++c) {
+          uint32_t v[32];
+          tmem_load32(lanes + 32 * c, v);
+          tmem_load_wait();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_shared(chunk_address(stage, lane, q), v[4 * q], v[4 * q + 1], v[4 * q + 2],
+                      v[4 * q + 3]);
+          __syncwarp();
+          const int col = col0 + 32 * c + 4 * (lane & 7);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int r = 4 * q + (lane >> 3), row = row0 + r;
+            const uint4 u = ld_shared(chunk_address(stage, r, lane & 7));
+            const float x[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                __uint_as_float(u.w)};
+            if (row < M && col < N)
+              write_out(g, (int64_t)it.z * g.batch_stride + (int64_t)row * g.ldo + col, N - col, x,
+                        alpha);
+          }
+          __syncwarp();
         }
       }
-      // This CTA's output is in memory: tell the grid. One thread decides for
-      // the four warps whether to go on.
-      if (lane == 0) tma_store_wait_all();
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
-      if (warp == 2 && lane == 0) {
-        // A CTA without a tile here must not count ahead of the others.
-        const bool go = !last && grid_wait(g, ph, stop_v) && *stop_v == 0;
-        epilogue_go = go;
-        if (go) {
-          __threadfence();
-          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.barrier) : "memory");
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2 && rank != 0)
+          mbar_arrive_cluster(peer_address(smem_u32(&acc_empty[acc]), 0));
+        else
+          mbar_arrive(smem_u32(&acc_empty[acc]));
+        if (!it.last) {
+          // This warp's part of the tile is in memory: count it.
+          tma_store_wait_all();
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.counters + it.z)
+                       : "memory");
         }
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
-      ok = epilogue_go != 0;
+      __syncwarp();
     }
-    for (uint32_t b = 0; b < 2; ++b)
-      if (asked >> b & 1u)
-        mbar_drain(smem_u32(&addend_full[warp - 2][b]), (parity >> b) & 1u);
+    for (int c = 0; c < kChunks; ++c)
+      if (asked >> c & 1u)
+        mbar_drain(smem_u32(&addend_full[warp - 2][c]), (parity >> c) & 1u);
   }
   __syncwarp();
   fence_before();
@@ -810,14 +814,14 @@ cudaError_t resident_ctas(int* out) {
     return cudaSuccess;
   }
   auto kernel = ns_kernel<CG, BN>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<BN>::smem);
   if (e != cudaSuccess) return e;
   int n = 0;
   if (CG == 2) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = Ring<BN>::smem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -828,7 +832,7 @@ cudaError_t resident_ctas(int* out) {
     n *= 2;
   } else {
     int sms = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, kSmem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, Ring<BN>::smem);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     n *= sms;
   }
@@ -847,7 +851,7 @@ cudaError_t run(const Maps& maps, const MuonNs& g, int64_t tiles, cudaStream_t s
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(most, tiles * CG));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = Ring<BN>::smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
