@@ -10,8 +10,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmua.so")
 SOURCES = ["mua_api.cu", "mua_select_warp.cu", "mua_apply.cu", "mua_fused.cu",
            os.path.join("muon", "muon_api.cu"), os.path.join("muon", "muon_momentum.cu"),
-           os.path.join("muon", "muon_ns.cu")]
-HEADERS = ["mua_kernels.cuh", os.path.join("muon", "muon.cuh"), os.path.join("..", "..", "include", "mua.h")]
+           os.path.join("muon", "muon_ns.cu"), os.path.join("muon", "muon_small.cu")]
+HEADERS = ["mua_kernels.cuh", os.path.join("muon", "muon.cuh"),
+           os.path.join("muon", "muon_tc.cuh"), os.path.join("muon", "muon_quant.cuh"), os.path.join("..", "..", "include", "mua.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -109,4 +109,13 @@ struct MuonNs {
 
 cudaError_t muon_launch_ns(const MuonStack& m, const MuonNs& g, cudaStream_t st);
 
+// Matrices that fit a CTA's shared memory: the whole operator in one launch, a
+// CTA each. Shared memory it takes, 0 where a matrix does not fit.
+uint32_t muon_small_smem(int32_t rows, int32_t cols);
+cudaError_t muon_launch_small(const MuonShape& s, const MuonNs& g, const MuonView& x, float eps,
+                              int e0, cudaStream_t st);
+cudaError_t muon_launch_small_step(const MuonShape& s, const MuonNs& g, const MuonQuant& q,
+                                   const void* grads, int g_type, float beta, int nesterov,
+                                   const MuonRandom& rnd, float eps, int e0, cudaStream_t st);
+
 }  // namespace mua

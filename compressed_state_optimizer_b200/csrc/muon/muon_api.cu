@@ -23,6 +23,7 @@ struct mua_muon_ctx {
   int32_t rows, cols, count, bits, steps;
   int32_t s;                 // short side: A and P are s x s
   bool tall;                 // rows > cols
+  bool small;                // one CTA holds a matrix on chip
   int32_t ld, lds;           // fp16 row strides of X and of A, P
   int32_t group, parts;
   int64_t bpm;               // blocks of one matrix
@@ -130,17 +131,9 @@ uint32_t* counters(const mua_muon_ctx* h, uint8_t* ws) {
   return reinterpret_cast<uint32_t*>(ws + h->off_counters);
 }
 
-// The Newton-Schulz steps of matrices first .. first + count - 1, X_0 and its
-// factors being in the workspace.
-int iterate(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count, const Target& to,
-            uint32_t* status, cudaStream_t st) {
-  mua::MuonStack m;
-  m.x[0] = ws + h->off_x[0];
-  m.x[1] = ws + h->off_x[1];
-  m.a = ws + h->off_a;
-  m.p = ws + h->off_p;
-  m.ld = h->ld;
-  m.lds = h->lds;
+// The iteration of matrices first .. first + count - 1.
+mua::MuonNs iteration(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count,
+                      const Target& to, uint32_t* status) {
   mua::MuonNs g;
   std::memset(&g, 0, sizeof g);
   g.rows = h->rows;
@@ -171,7 +164,21 @@ int iterate(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count, co
   g.counters = counters(h, ws);
   g.status = status;
   g.wait_ns = (uint64_t)std::max<int64_t>(0, h->wait_ns);
-  const cudaError_t e = mua::muon_launch_ns(m, g, st);
+  return g;
+}
+
+// Its launch, X_0 and its factors being in the workspace.
+int iterate(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count, const Target& to,
+            uint32_t* status, cudaStream_t st) {
+  mua::MuonStack m;
+  m.x[0] = ws + h->off_x[0];
+  m.x[1] = ws + h->off_x[1];
+  m.a = ws + h->off_a;
+  m.p = ws + h->off_p;
+  m.ld = h->ld;
+  m.lds = h->lds;
+  const cudaError_t e =
+      mua::muon_launch_ns(m, iteration(h, ws, first, count, to, status), st);
   return e == cudaSuccess ? MUA_OK : fail(e, "Newton-Schulz kernel launch");
 }
 
@@ -213,6 +220,7 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
   }
   h->s = s;
   h->tall = rows > cols;
+  h->small = mua::muon_small_smem(rows, cols) > 0;
   h->ld = (int32_t)round_up(cols, 8);
   h->lds = (int32_t)round_up(s, 8);
   h->bpm = bpm;
@@ -335,6 +343,14 @@ int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   double* partials = reinterpret_cast<double*>(ws + h->off_partials);
   const Target to = {false, out, MUA_BF16, out_matrix_stride, out_row_stride, 1.0, 0.0f};
+  uint32_t* status = reinterpret_cast<uint32_t*>(ws) + mua::kMuonHdrStatus;
+  if (h->small) {
+    const mua::MuonView v = {const_cast<void*>(x), x_type, x_matrix_stride, x_row_stride};
+    const cudaError_t e =
+        mua::muon_launch_small(shape(h, h->count), iteration(h, ws, 0, h->count, to, status), v,
+                               eps, h->ex[0], st);
+    return e == cudaSuccess ? MUA_OK : fail(e, "orthogonalization kernel launch");
+  }
   for (int32_t first = 0; first < h->count; first += h->group) {
     const int32_t count = std::min(h->group, h->count - first);
     const mua::MuonView v = {
@@ -345,8 +361,7 @@ int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t 
     e = mua::muon_launch_load(shape(h, count), v, partials, eps, h->ex[0], ws + h->off_x[0],
                               reinterpret_cast<float*>(ws + h->off_factor), counters(h, ws), st);
     if (e != cudaSuccess) return fail(e, "load kernel launch");
-    const int rc = iterate(h, ws, first, count, to,
-                           reinterpret_cast<uint32_t*>(ws) + mua::kMuonHdrStatus, st);
+    const int rc = iterate(h, ws, first, count, to, status, st);
     if (rc != MUA_OK) return rc;
   }
   return MUA_OK;
@@ -371,6 +386,13 @@ int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* g
   const int64_t n = (int64_t)h->rows * h->cols;
   const Target to = {true, params, params_type, n, h->cols,
                      (double)lr * (double)scale, (float)(1.0 - (double)lr * (double)wd)};
+  uint32_t* status = static_cast<uint32_t*>(state) + mua::kMuonHdrStatus;
+  if (h->small) {
+    const cudaError_t e = mua::muon_launch_small_step(
+        shape(h, h->count), iteration(h, ws, 0, h->count, to, status), quant(h, state, 0), grads,
+        grads_type, beta, nesterov != 0, random_keys(h, 0, t, seed), eps, h->ex[0], st);
+    return e == cudaSuccess ? MUA_OK : fail(e, "step kernel launch");
+  }
   for (int32_t first = 0; first < h->count; first += h->group) {
     const int32_t count = std::min(h->group, h->count - first);
     const mua::MuonShape s = shape(h, count);
@@ -383,8 +405,7 @@ int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* g
                                   random_keys(h, first, t, seed), nullptr, 0, partials, eps,
                                   h->ex[0], ws + h->off_x[0], factor, counters(h, ws), st);
     if (e != cudaSuccess) return fail(e, "momentum kernel launch");
-    const int rc = iterate(h, ws, first, count, to,
-                           static_cast<uint32_t*>(state) + mua::kMuonHdrStatus, st);
+    const int rc = iterate(h, ws, first, count, to, status, st);
     if (rc != MUA_OK) return rc;
   }
   return MUA_OK;

@@ -1,0 +1,415 @@
+// Matrices whose iteration fits one SM: the whole operator in one launch, a CTA
+// per matrix. X, A and P stay in shared memory as fp16 tiles in the layout the
+// MMAs read (128-byte swizzled rows of 64 elements), accumulators in TMEM;
+// global memory is read once or twice at the start and written once at the end.
+//
+// Each of the 3 products per step is a handful of MMAs followed by an epilogue
+// of all 16 warps, so a step is bound by the latency of issue, completion,
+// TMEM read and CTA barrier, not by arithmetic. X has the caller's orientation
+// (s = short, l = long side): a wide one is s rows of ceil(l / 64) chunks, a
+// tall one l rows of ceil(s / 64) chunks, rows and contracted columns padded
+// with zeros to 16. An MMA always covers 128 rows; those behind the last are
+// whatever shared memory holds there, and only make accumulator rows that
+// nothing reads.
+#include "muon_quant.cuh"
+
+#include <algorithm>
+
+namespace mua {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr uint32_t kOverread = 16384;  // 128 rows of a chunk that starts at its last row
+
+__host__ __device__ __forceinline__ int round16(int x) { return (x + 15) & ~15; }
+
+struct Plan {
+  int s, l, s16, l16;     // short and long side, padded
+  bool tall;
+  int ns, chunks;         // 64-wide chunks of the short side; of X
+  uint32_t xs, ps;        // bytes of a chunk of X, of A and P
+  uint32_t a_off, p_off, bytes;
+  uint32_t columns;       // of TMEM
+};
+__host__ __device__ __forceinline__ Plan plan_of(int rows, int cols) {
+  Plan p;
+  p.tall = rows > cols;
+  p.s = p.tall ? cols : rows;
+  p.l = p.tall ? rows : cols;
+  p.s16 = round16(p.s);
+  p.l16 = round16(p.l);
+  p.ns = (p.s + 63) / 64;
+  p.chunks = p.tall ? p.ns : (p.l + 63) / 64;
+  p.xs = (uint32_t)(p.tall ? p.l16 : p.s16) * 128u;
+  p.ps = (uint32_t)p.s16 * 128u;
+  p.a_off = (uint32_t)p.chunks * p.xs;
+  p.p_off = p.a_off + (uint32_t)p.ns * p.ps;
+  p.bytes = p.p_off + (uint32_t)p.ns * p.ps + kOverread;
+  const int update = p.tall ? (p.l + 127) / 128 * p.s16 : p.l16;
+  const int need = update > 512 ? 512 : (update > p.s16 ? update : p.s16);
+  p.columns = 32;
+  while ((int)p.columns < need) p.columns *= 2;
+  return p;
+}
+
+// Address of the 16-byte group holding (row, col .. col + 7) of a chunked tile.
+__device__ __forceinline__ uint32_t group_address(uint32_t tile, uint32_t chunk_bytes, int row,
+                                                  int col) {
+  return chunk_address(tile + (uint32_t)(col >> 6) * chunk_bytes, row, (col >> 3) & 7);
+}
+
+// SRC: 0 fp32 and 1 bf16 matrices to orthogonalize; 2 + type + 2 (4 bits) a step.
+template <int SRC>
+__global__ void __launch_bounds__(kThreads, 1)
+small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQuant Q,
+             const void* grads, float beta, int nesterov, const __grid_constant__ MuonRandom rnd,
+             float eps, int e0) {
+  constexpr bool STEP = SRC >= 2;
+  constexpr int T = SRC & 1;                       // value type of x or the gradients
+  constexpr int BITS = SRC >= 4 ? 4 : 8;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t done;
+  __shared__ uint32_t tmem_base_s, stop;
+  __shared__ NormScale scale_s;
+  const Plan p = plan_of(sh.rows, sh.cols);
+  const uint32_t X = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t A = X + p.a_off, P = X + p.p_off;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t mat = blockIdx.x;
+  const int64_t n = (int64_t)sh.rows * sh.cols;
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&done), 1);
+    stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_base_s)),
+                 "r"(p.columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // Rows and columns that pad a side to 16 hold zeros throughout.
+  if (((p.s | p.l) & 15) != 0)
+    for (uint32_t o = threadIdx.x * 16; o < p.a_off; o += kThreads * 16)
+      st_shared(X + o, 0u, 0u, 0u, 0u);
+
+  // The norm, then X_0 = x 2^(e0 - t): see muon_launch_load.
+  if constexpr (!STEP) {
+    const int es = T == kBf16 ? 2 : 4;
+    const uint8_t* xm = static_cast<const uint8_t*>(x.p) + mat * x.matrix_stride * es;
+    const bool vec = aligned16(xm) && (x.row_stride * es) % 16 == 0;
+    const uint32_t per_row = (uint32_t)(sh.cols + 7) / 8, groups = per_row * (uint32_t)sh.rows;
+    double sum = 0.0;
+    for (uint32_t q = threadIdx.x; q < groups; q += kThreads) {
+      const uint32_t row = q / per_row, col = 8 * (q - row * per_row);
+      float v[8];
+      load8<T>(xm + (int64_t)row * x.row_stride * es, col, sh.cols, vec, v);
+      sum += sum_squares(v);
+    }
+    sum = cta_sum<kThreads>(sum);
+    if (threadIdx.x == 0) scale_s = scale_of(sum, eps, e0);
+    __syncthreads();
+    const NormScale ns = scale_s;
+    for (uint32_t q = threadIdx.x; q < groups; q += kThreads) {
+      const uint32_t row = q / per_row, col = 8 * (q - row * per_row);
+      float v[8];
+      load8<T>(xm + (int64_t)row * x.row_stride * es, col, sh.cols, vec, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * ns.first * ns.second;
+      st_shared(group_address(X, p.xs, (int)row, (int)col), pack_f16(v[0], v[1]),
+                pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+    }
+  } else {
+    const int half = threadIdx.x >> 4, sub = threadIdx.x & 15;
+    const uint8_t* gm = static_cast<const uint8_t*>(grads) + mat * n * (T == kBf16 ? 2 : 4);
+    const bool vec = aligned16(gm);
+    const int64_t base = mat * Q.bpm;
+    double sum = 0.0;
+    for (int64_t b = half; b < Q.bpm; b += kThreads / 16) {
+      float q[8], m[8], u[8], gv[8];
+      load8<T>(gm, b * kMuonBlock + 8 * sub, n, vec, gv);
+      unpack8<BITS>(load_codes<BITS>(Q.codes, base + b, sub), q);
+      new_momentum(q, Q.scales[base + b], gv, beta, nesterov, m, u);
+      sum += sum_squares(u);
+    }
+    sum = cta_sum<kThreads>(sum);
+    if (threadIdx.x == 0) scale_s = scale_of(sum, eps, e0);
+    __syncthreads();
+    const NormScale ns = scale_s;
+    bool bad = false;
+    for (int64_t b0 = 2 * warp; b0 < Q.bpm; b0 += kThreads / 16) {
+      const int64_t b = b0 + (half & 1);
+      const bool live = b < Q.bpm;
+      const int64_t i = b * kMuonBlock + 8 * sub;
+      float q[8], m[8], u[8], gv[8];
+      load8<T>(gm, i, n, vec, gv);
+      uint2 codes = make_uint2(0u, 0u);
+      float scale = 0.0f;
+      if (live) {
+        codes = load_codes<BITS>(Q.codes, base + b, sub);
+        scale = Q.scales[base + b];
+      }
+      unpack8<BITS>(codes, q);
+      new_momentum(q, scale, gv, beta, nesterov, m, u);
+      uint32_t c[8];
+      quantize_block<BITS>(m, i, n, (uint64_t)(rnd.base + (base + b) * kMuonBlock) / 8 + sub, rnd,
+                           scale, c, bad);
+      if (live) {
+        store_codes<BITS>(Q.codes, base + b, sub, c);
+        if (sub == 0) Q.scales[base + b] = scale;
+        int row = (int)((uint32_t)i / (uint32_t)sh.cols);
+        int col = (int)i - row * sh.cols;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = u[e] * ns.first * ns.second;
+        if ((sh.cols & 7) == 0) {  // eight values of one row
+          if (i < n)
+            st_shared(group_address(X, p.xs, row, col), pack_f16(u[0], u[1]),
+                      pack_f16(u[2], u[3]), pack_f16(u[4], u[5]), pack_f16(u[6], u[7]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (i + e < n)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(group_address(X, p.xs, row, col) +
+                                                           2u * (col & 7)),
+                           "h"(__half_as_ushort(__float2half_rn(u[e])))
+                           : "memory");
+            if (++col == sh.cols) {
+              col = 0;
+              ++row;
+            }
+          }
+        }
+      }
+    }
+    if (bad) atomicOr(Q.status, kMuonNonFinite);
+  }
+  fence_async_shared();
+  fence_before();
+  __syncthreads();
+  fence_after();
+
+  const uint32_t tmem = tmem_base_s;
+  const float factor = scale_s.factor;
+  const int quarter = warp & 3, part = warp >> 2;     // TMEM lanes; every fourth 16 columns
+  const int lane_row = quarter * 32 + lane;
+  const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+  const int sunits = p.s16 / 16;
+  volatile uint32_t* stop_v = &stop;
+  uint32_t turn = 0;
+  bool ok = true;
+  // Waits for the MMAs issued; false (in every thread) when the CTA gives up.
+  auto finish = [&]() {
+    const bool mine = mbar_wait(smem_u32(&done), turn, g.wait_ns, stop_v);
+    ok = __syncthreads_or(!mine) == 0;
+    fence_after();
+    if (ok) turn ^= 1u;
+    return ok;
+  };
+  // Every thread's tile writes and TMEM reads come before the next MMAs.
+  auto publish = [&]() {
+    fence_async_shared();
+    fence_before();
+    __syncthreads();
+    fence_after();
+  };
+
+  for (int k = 0; ok && k < g.steps; ++k) {
+    // A = f^2 X X^T
+    if (warp == 0 && elect_one()) {
+      const uint32_t idesc = instruction_desc<1>(p.s16, p.tall, p.tall);
+      if (p.tall) {
+        // 64 further rows of A behind a single chunk: the chunk again.
+        const uint32_t lead = p.ns > 1 ? p.xs : 0;
+        for (int kk = 0; kk < p.l16 / 16; ++kk) {
+          const uint64_t d = operand_desc(X + kk * 2048, lead);
+          mma_f16<1>(tmem, d, d, idesc, kk != 0);
+        }
+      } else {
+        for (int kk = 0; kk < p.l16 / 16; ++kk) {
+          const uint64_t d = operand_desc(X + (kk >> 2) * p.xs + (kk & 3) * 32, 16);
+          mma_f16<1>(tmem, d, d, idesc, kk != 0);
+        }
+      }
+      mma_commit<1>(smem_u32(&done));
+    }
+    __syncwarp();
+    if (!finish()) break;
+    if (quarter * 32 < p.s16) {
+      const float alpha = k == 0 ? g.gram_alpha[0] * factor * factor : g.gram_alpha[k];
+      for (int u = part; u < sunits; u += 4) {
+        uint32_t v[16];
+        tmem_load16(lanes + 16 * u, v);
+        tmem_load_wait();
+        if (lane_row < p.s16) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_f16(__uint_as_float(v[8 * h + 2 * e]) * alpha,
+                              __uint_as_float(v[8 * h + 2 * e + 1]) * alpha);
+            st_shared(group_address(A, p.ps, lane_row, 16 * u + 8 * h), w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    publish();
+
+    // P = a I + b A + c A A
+    if (warp == 0 && elect_one()) {
+      const uint32_t idesc = instruction_desc<1>(p.s16, false, false);
+      for (int kk = 0; kk < sunits; ++kk) {
+        const uint64_t d = operand_desc(A + (kk >> 2) * p.ps + (kk & 3) * 32, 16);
+        mma_f16<1>(tmem, d, d, idesc, kk != 0);
+      }
+      mma_commit<1>(smem_u32(&done));
+    }
+    __syncwarp();
+    if (!finish()) break;
+    if (quarter * 32 < p.s16) {
+      const float alpha = g.poly_alpha[k], mid = g.poly_mid[k], diag = g.poly_diag[k];
+      for (int u = part; u < sunits; u += 4) {
+        uint32_t v[16];
+        tmem_load16(lanes + 16 * u, v);
+        tmem_load_wait();
+        if (lane_row < p.s16) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = 16 * u + 8 * h;
+            const uint4 a = ld_shared(group_address(A, p.ps, lane_row, col));
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
+              float x0 = fmaf(y.x, mid, __uint_as_float(v[8 * h + 2 * e]) * alpha);
+              float x1 = fmaf(y.y, mid, __uint_as_float(v[8 * h + 2 * e + 1]) * alpha);
+              if (col + 2 * e == lane_row && lane_row < p.s) x0 += diag;
+              if (col + 2 * e + 1 == lane_row && lane_row < p.s) x1 += diag;
+              w[e] = pack_f16(x0, x1);
+            }
+            st_shared(group_address(P, p.ps, lane_row, col), w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    publish();
+
+    // X' = f P X (X P), 512 accumulator columns at a time; a pass replaces only
+    // the columns (rows) of X that no other pass reads.
+    const bool last = k == g.steps - 1;
+    const float alpha = k == 0 ? g.update_alpha[0] * factor : g.update_alpha[k];
+    const int tiles = p.tall ? (p.l + 127) / 128 : 1;
+    const int pass = p.tall ? 512 / p.s16 : 512;      // tiles, or columns
+    const int total = p.tall ? tiles : p.l16;
+    for (int p0 = 0; p0 < total; p0 += pass) {
+      const int now = min(pass, total - p0);
+      if (warp == 0 && elect_one()) {
+        if (p.tall) {
+          const uint32_t idesc = instruction_desc<1>(p.s16, false, false);
+          for (int t = 0; t < now; ++t)
+            for (int kk = 0; kk < sunits; ++kk)
+              mma_f16<1>(tmem + t * p.s16,
+                         operand_desc(X + (kk >> 2) * p.xs + (p0 + t) * 16384 + (kk & 3) * 32, 16),
+                         operand_desc(P + (kk >> 2) * p.ps + (kk & 3) * 32, 16), idesc, kk != 0);
+        } else {
+          for (int n0 = 0; n0 < now; n0 += 256) {
+            const uint32_t idesc = instruction_desc<1>(min(256, now - n0), false, true);
+            for (int kk = 0; kk < sunits; ++kk)
+              mma_f16<1>(tmem + n0, operand_desc(P + (kk >> 2) * p.ps + (kk & 3) * 32, 16),
+                         operand_desc(X + ((p0 + n0) >> 6) * p.xs + kk * 2048, p.xs), idesc,
+                         kk != 0);
+          }
+        }
+        mma_commit<1>(smem_u32(&done));
+      }
+      __syncwarp();
+      if (!finish()) break;
+      const int units = p.tall ? now * sunits : now / 16;
+      for (int u = part; u < units; u += 4) {
+        const int t = p.tall ? u / sunits : 0;
+        const int row0 = p.tall ? (p0 + t) * 128 + quarter * 32 : quarter * 32;
+        const int col = p.tall ? 16 * (u - t * sunits) : p0 + 16 * u;
+        if (row0 >= (p.tall ? p.l16 : p.s16)) continue;
+        uint32_t v[16];
+        tmem_load16(lanes + 16 * u, v);
+        tmem_load_wait();
+        const int row = row0 + lane;
+        if (!last) {
+          if (row < (p.tall ? p.l16 : p.s16)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_f16(__uint_as_float(v[8 * h + 2 * e]) * alpha,
+                                __uint_as_float(v[8 * h + 2 * e + 1]) * alpha);
+              st_shared(group_address(X, p.xs, row, col + 8 * h), w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else if (row < sh.rows) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const float y[4] = {__uint_as_float(v[4 * h]), __uint_as_float(v[4 * h + 1]),
+                                __uint_as_float(v[4 * h + 2]), __uint_as_float(v[4 * h + 3])};
+            if (col + 4 * h < sh.cols)
+              write_out(g, mat * g.batch_stride + (int64_t)row * g.ldo + col + 4 * h,
+                        sh.cols - col - 4 * h, y, alpha);
+          }
+        }
+        __syncwarp();
+      }
+      publish();
+    }
+  }
+  // MMAs in flight end before shared memory and TMEM go.
+  if (!ok) mbar_drain(smem_u32(&done), turn);
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(p.columns));
+  if (threadIdx.x == 0 && stop) atomicOr(g.status, kMuonTimeout);
+}
+
+template <int SRC>
+cudaError_t run(const MuonShape& s, const MuonNs& g, const MuonView& x, const MuonQuant& q,
+                const void* grads, float beta, int nesterov, const MuonRandom& rnd, float eps,
+                int e0, cudaStream_t st) {
+  auto kernel = small_kernel<SRC>;
+  const uint32_t smem = muon_small_smem(s.rows, s.cols);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)s.count, kThreads, smem, st>>>(s, g, x, q, grads, beta, nesterov, rnd, eps, e0);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+uint32_t muon_small_smem(int32_t rows, int32_t cols) {
+  if (std::min(rows, cols) > 128 || std::max(rows, cols) > 8192) return 0;
+  const uint32_t bytes = plan_of(rows, cols).bytes + 1024;  // + alignment
+  return bytes <= 230000 ? bytes : 0;
+}
+
+cudaError_t muon_launch_small(const MuonShape& s, const MuonNs& g, const MuonView& x, float eps,
+                              int e0, cudaStream_t st) {
+  const MuonQuant q = {};
+  const MuonRandom r = {};
+  return x.type == kBf16 ? run<1>(s, g, x, q, nullptr, 0.0f, 0, r, eps, e0, st)
+                         : run<0>(s, g, x, q, nullptr, 0.0f, 0, r, eps, e0, st);
+}
+
+cudaError_t muon_launch_small_step(const MuonShape& s, const MuonNs& g, const MuonQuant& q,
+                                   const void* grads, int g_type, float beta, int nesterov,
+                                   const MuonRandom& rnd, float eps, int e0, cudaStream_t st) {
+  const MuonView x = {};
+  auto k = q.bits == 8 ? (g_type == kBf16 ? run<3> : run<2>) : (g_type == kBf16 ? run<5> : run<4>);
+  return k(s, g, x, q, grads, beta, nesterov, rnd, eps, e0, st);
+}
+
+}  // namespace mua
