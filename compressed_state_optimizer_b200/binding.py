@@ -352,7 +352,7 @@ class Muon:
 
     def _buffer(self, x, size, what):
         import torch
-        if x.dtype != torch.uint8 or not x.is_contiguous() or x.numel() < size:
+        if x.dtype is not torch.uint8 or x.numel() < size or not x.is_contiguous():
             raise ValueError(f"{what}: a contiguous uint8 tensor of at least {size} bytes")
 
     def _stack(self, x, what):
@@ -365,21 +365,30 @@ class Muon:
         row = x.stride(-2) if self.rows > 1 else self.cols
         return (x.stride(0) if self.count > 1 else self.rows * row), row
 
-    @staticmethod
-    def _device(stream, *tensors, params=None):
-        """The tensors' CUDA device and the stream's pointer on it."""
+    def _launch(self, name, stream, tensors, args, params=None):
+        """Call ``name(handle, *args, stream)`` on the tensors' device."""
         import torch
-        dev = tensors[0].device
+        index = tensors[0].get_device()
+        grad = torch.is_grad_enabled()
         for x in tensors:
-            if not x.is_cuda or x.device != dev:
+            if x.get_device() != index or index < 0:
                 raise ValueError("tensors must be on one CUDA device")
-            if x.requires_grad and torch.is_grad_enabled() and x is not params:
+            if grad and x.requires_grad and x is not params:
                 raise ValueError("not differentiable: detach() the tensors")
         if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-        return torch.cuda.device(dev), stream.cuda_stream
+            s = torch._C._cuda_getCurrentRawStream(index)
+        elif stream.device.index == index:
+            s = stream.cuda_stream
+        else:
+            raise ValueError(f"stream on {stream.device}, tensors on cuda:{index}")
+        fn = getattr(library(), name)
+        if torch.cuda.current_device() == index:
+            code = fn(self._h, *args, s)
+        else:
+            with torch.cuda.device(index):
+                code = fn(self._h, *args, s)
+        if code != MUA_OK:
+            raise MuaError(code, name)
 
     # ------------------------------------------------------------ operators
     def momentum(self, grads, state, direction, *, beta, nesterov=True, t, seed, stream=None):
@@ -387,29 +396,23 @@ class Muon:
         ``state``, the direction to ``direction`` (fp32 or bf16)."""
         gt, dt = self._values(grads, "grads"), self._values(direction, "direction")
         self._buffer(state, self.state_bytes, "state")
-        device, s = self._device(stream, grads, state, direction)
-        with device:
-            _check(library().mua_muon_momentum(self._h, grads.data_ptr(), gt, state.data_ptr(),
-                                               direction.data_ptr(), dt, beta, int(nesterov), t,
-                                               seed, s), "mua_muon_momentum")
+        self._launch("mua_muon_momentum", stream, (grads, state, direction),
+                     (grads.data_ptr(), gt, state.data_ptr(), direction.data_ptr(), dt, beta,
+                      nesterov, t, seed))
 
     def read_momentum(self, state, out, stream=None):
         """The momentum's values to ``out`` (fp32 or bf16)."""
         ot = self._values(out, "out")
         self._buffer(state, self.state_bytes, "state")
-        device, s = self._device(stream, state, out)
-        with device:
-            _check(library().mua_muon_read(self._h, state.data_ptr(), out.data_ptr(), ot, s),
-                   "mua_muon_read")
+        self._launch("mua_muon_read", stream, (state, out),
+                     (state.data_ptr(), out.data_ptr(), ot))
 
     def write_momentum(self, values, state, stream=None):
         """``values`` (fp32 or bf16) as the momentum, each to the nearest level."""
         vt = self._values(values, "values")
         self._buffer(state, self.state_bytes, "state")
-        device, s = self._device(stream, values, state)
-        with device:
-            _check(library().mua_muon_write(self._h, values.data_ptr(), vt, state.data_ptr(), s),
-                   "mua_muon_write")
+        self._launch("mua_muon_write", stream, (values, state),
+                     (values.data_ptr(), vt, state.data_ptr()))
 
     def orthogonalize(self, x, out, workspace, *, eps=1e-7, stream=None):
         """Newton-Schulz orthogonalisation of the matrices ``x`` ([count, rows,
@@ -422,12 +425,9 @@ class Muon:
         if out.dtype != torch.bfloat16:
             raise ValueError(f"out: bfloat16, not {out.dtype}")
         self._buffer(workspace, self.workspace_bytes, "workspace")
-        device, s = self._device(stream, x, out, workspace)
-        with device:
-            _check(library().mua_muon_orthogonalize(self._h, x.data_ptr(), xt, xs, xr,
-                                                    out.data_ptr(), os_, orow,
-                                                    workspace.data_ptr(), eps, s),
-                   "mua_muon_orthogonalize")
+        self._launch("mua_muon_orthogonalize", stream, (x, out, workspace),
+                     (x.data_ptr(), xt, xs, xr, out.data_ptr(), os_, orow, workspace.data_ptr(),
+                      eps))
 
     def step(self, params, grads, state, workspace, *, lr, beta=0.95, eps=1e-7, wd=0.0,
              scale=None, nesterov=True, t, seed, stream=None):
@@ -439,11 +439,10 @@ class Muon:
         pt, gt = self._values(params, "params"), self._values(grads, "grads")
         self._buffer(state, self.state_bytes, "state")
         self._buffer(workspace, self.workspace_bytes, "workspace")
-        device, s = self._device(stream, params, grads, state, workspace, params=params)
-        with device:
-            _check(library().mua_muon_step(self._h, params.data_ptr(), pt, grads.data_ptr(), gt,
-                                           state.data_ptr(), workspace.data_ptr(), lr, scale, beta,
-                                           int(nesterov), eps, wd, t, seed, s), "mua_muon_step")
+        self._launch("mua_muon_step", stream, (params, grads, state, workspace),
+                     (params.data_ptr(), pt, grads.data_ptr(), gt, state.data_ptr(),
+                      workspace.data_ptr(), lr, scale, beta, nesterov, eps, wd, t, seed),
+                     params=params)
 
     def set_wait_limit_ns(self, ns: int):
         """Bound on a wait inside the matrix-product kernels (<= 0: give up at once)."""
@@ -454,9 +453,11 @@ class Muon:
         """Status bits of a state (``step``, ``momentum``) or of a workspace
         (``orthogonalize``)."""
         self._buffer(buffer, 256, "buffer")
-        device, s = self._device(stream, buffer)
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(buffer.device)
         out = ctypes.c_int32()
-        with device:
-            _check(library().mua_muon_get_status(self._h, buffer.data_ptr(), s,
+        with torch.cuda.device(buffer.device):
+            _check(library().mua_muon_get_status(self._h, buffer.data_ptr(), stream.cuda_stream,
                                                  ctypes.byref(out)), "mua_muon_get_status")
         return int(out.value)

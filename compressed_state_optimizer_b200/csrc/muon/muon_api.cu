@@ -194,7 +194,7 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
       n >= (1ll << 31))
     return MUA_ERR_UNSUPPORTED;
   const int64_t bpm = (n + mua::kMuonBlock - 1) / mua::kMuonBlock;
-  if ((int64_t)count * ((bpm + 63) / 64) >= (1ll << 31)) return MUA_ERR_UNSUPPORTED;
+  if ((int64_t)count * ((bpm + 31) / 32) >= (1ll << 31)) return MUA_ERR_UNSUPPORTED;
 
   mua_muon_ctx* h = new (std::nothrow) mua_muon_ctx();
   if (!h) return MUA_ERR_ARG;

@@ -12,8 +12,8 @@ namespace mua {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;                          // blocks per half-warp
-constexpr int kChunkBlocks = kThreads / 16 * kUnroll;  // 64 blocks (8192 values) per CTA
+constexpr int kUnroll = 2;                             // blocks per half-warp
+constexpr int kChunkBlocks = kThreads / 16 * kUnroll;  // 32 blocks (4096 values) per CTA
 
 __device__ __forceinline__ void wait_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -24,7 +24,7 @@ __device__ __forceinline__ void release_next() {
 
 // ---------------------------------------------------------------- kernels
 
-// Grid: splits x count CTAs, a CTA takes 64 consecutive blocks of one matrix.
+// Grid: splits x count CTAs, a CTA takes 32 consecutive blocks of one matrix.
 // OUT: 0 fp32, 1 bf16 (contiguous), 2 fp16 X_0 with row stride ld.
 template <int BITS, int G, int OUT>
 __global__ void __launch_bounds__(kThreads)
@@ -74,7 +74,7 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
     const int64_t i = b * kMuonBlock + 8 * sub;
     float new_scale;
     uint32_t c[8];
-    quantize_block<BITS>(m, i, n, (uint64_t)(rnd.base + (base + b) * kMuonBlock) / 8 + sub, rnd,
+    quantize_block<BITS>(m, left_of(i, n), (uint64_t)(rnd.base + (base + b) * kMuonBlock) / 8 + sub, rnd,
                          new_scale, c, bad);
     if (b < Q.bpm) {
       store_codes<BITS>(Q.codes, base + b, sub, c);
@@ -240,13 +240,13 @@ write_kernel(MuonShape s, MuonQuant Q, const void* values, int splits) {
     const int64_t b = (int64_t)split * kChunkBlocks + half + k * (kThreads / 16);
     float v[8];
     load8<T>(vm, b * kMuonBlock + 8 * sub, n, vec, v);
-    uint32_t top = 0;
+    float top = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    for (int e = 0; e < 8; ++e) top = max_magnitude(top, v[e]);
     top = half_warp_max(top);
     float scale, inverse;
     block_scale(top, Level<BITS>::recip, scale, inverse);
-    bad = bad || top >= 0x7F800000u;
+    bad = bad || !(top < __uint_as_float(0x7F800000u));
     uint32_t c[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {

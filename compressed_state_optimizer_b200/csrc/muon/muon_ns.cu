@@ -414,6 +414,16 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
         // eight lanes a row's 128 (64) contiguous bytes.
 #pragma unroll 1
         for (int c = 0; c < 2 * chunks; ++c) {
+          const int col = col0 + 32 * c + 4 * (lane & 7);
+          const int64_t at0 = (int64_t)it.z * g.batch_stride +
+                              (int64_t)(row0 + (lane >> 3)) * g.ldo + col;
+          float4 old[8];  // all loads before the first store
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            old[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (row0 + 4 * q + (lane >> 3) < M && col < N)
+              old[q] = read_four(g, at0 + 4 * q * g.ldo, N - col);
+          }
           uint32_t v[32];
           tmem_load32(lanes + 32 * c, v);
           tmem_load_wait();
@@ -422,16 +432,13 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
             st_shared(chunk_address(stage, lane, q), v[4 * q], v[4 * q + 1], v[4 * q + 2],
                       v[4 * q + 3]);
           __syncwarp();
-          const int col = col0 + 32 * c + 4 * (lane & 7);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const int r = 4 * q + (lane >> 3), row = row0 + r;
+            const int r = 4 * q + (lane >> 3);
             const uint4 u = ld_shared(chunk_address(stage, r, lane & 7));
-            const float x[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
-                                __uint_as_float(u.w)};
-            if (row < M && col < N)
-              write_out(g, (int64_t)it.z * g.batch_stride + (int64_t)row * g.ldo + col, N - col, x,
-                        alpha);
+            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+            if (row0 + r < M && col < N)
+              write_four(g, at0 + 4 * q * g.ldo, N - col, old[q], x, alpha);
           }
           __syncwarp();
         }

@@ -124,12 +124,11 @@ __device__ __forceinline__ void store_codes(uint8_t* codes, int64_t block, int s
   }
 }
 
-// Scale and its reciprocal of a block whose largest magnitude has the bit
-// pattern top. A block below 2^-100 holds zeros: 1 / scale would overflow.
-// NaN and infinity order above every finite value as bits and stay in the scale.
-__device__ __forceinline__ void block_scale(uint32_t top, float level_recip, float& scale,
+// Scale and its reciprocal of a block whose largest magnitude is a. A block
+// below 2^-100 holds zeros: 1 / scale would overflow. NaN and infinity stay in
+// the scale.
+__device__ __forceinline__ void block_scale(float a, float level_recip, float& scale,
                                             float& inverse) {
-  const float a = __uint_as_float(top);
   scale = 0.0f;
   inverse = 0.0f;
   if (!(a < 7.8886090522101181e-31f)) {  // 2^-100
@@ -138,9 +137,15 @@ __device__ __forceinline__ void block_scale(uint32_t top, float level_recip, flo
   }
 }
 
-__device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
+// The larger magnitude, NaN if either is.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ float half_warp_max(float v) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  for (int o = 8; o > 0; o >>= 1) v = max_magnitude(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
 
@@ -161,23 +166,24 @@ __device__ __forceinline__ void new_momentum(const float (&q)[8], float scale, c
   }
 }
 
-// Scale and codes of a block's new momentum, this lane's 8 values being
-// i .. i + 7 of the matrix's n; all lanes of a warp call it.
+// Scale and codes of a block's new momentum, of which this lane holds 8 values,
+// `left` (8 or fewer) of them inside the matrix; all lanes of a warp call it.
 template <int BITS>
-__device__ __forceinline__ void quantize_block(float (&m)[8], int64_t i, int64_t n,
-                                               uint64_t counter, const MuonRandom& rnd,
-                                               float& scale, uint32_t (&c)[8], bool& bad) {
-  uint32_t top = 0;
+__device__ __forceinline__ void quantize_block(float (&m)[8], int left, uint64_t counter,
+                                               const MuonRandom& rnd, float& scale,
+                                               uint32_t (&c)[8], bool& bad) {
+  if (left < 8) {  // nothing is held behind the matrix's last value
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    // Behind the matrix's last value nothing is held (its codes are 0).
-    if (i + e >= n) m[e] = 0.0f;
-    top = max(top, __float_as_uint(m[e]) & 0x7FFFFFFFu);
+    for (int e = 0; e < 8; ++e)
+      if (e >= left) m[e] = 0.0f;
   }
+  float top = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max_magnitude(top, m[e]);
   top = half_warp_max(top);
   float inverse;
   block_scale(top, Level<BITS>::recip, scale, inverse);
-  bad = bad || top >= 0x7F800000u;
+  bad = bad || !(top < __uint_as_float(0x7F800000u));
   const uint4 w =
       philox4x32_10((uint32_t)counter, (uint32_t)(counter >> 32), rnd.t_lo, rnd.t_hi, rnd.keys);
 #pragma unroll
@@ -190,8 +196,16 @@ __device__ __forceinline__ void quantize_block(float (&m)[8], int64_t i, int64_t
                           Level<BITS>::value);
     const float z = __fadd_rd(y, __uint_as_float(0x3F800000u | r));
     c[e] = __float_as_uint(__fadd_rd(z, 12582911.0f));
-    if (i + e >= n) c[e] = 0;
   }
+  if (left < 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e >= left) c[e] = 0;
+  }
+}
+// Of n values, those from i on that a group of 8 holds (0 .. 8).
+__device__ __forceinline__ int left_of(int64_t i, int64_t n) {
+  return (int)(i + 8 <= n ? 8 : (i < n ? n - i : 0));
 }
 
 __device__ __forceinline__ double sum_squares(const float (&v)[8]) {

@@ -45,7 +45,7 @@ __host__ __device__ __forceinline__ Plan plan_of(int rows, int cols) {
   p.a_off = (uint32_t)p.chunks * p.xs;
   p.p_off = p.a_off + (uint32_t)p.ns * p.ps;
   p.bytes = p.p_off + (uint32_t)p.ns * p.ps + kOverread;
-  const int update = p.tall ? (p.l + 127) / 128 * p.s16 : p.l16;
+  const int update = (p.l + 127) / 128 * p.s16;
   const int need = update > 512 ? 512 : (update > p.s16 ? update : p.s16);
   p.columns = 32;
   while ((int)p.columns < need) p.columns *= 2;
@@ -56,6 +56,11 @@ __host__ __device__ __forceinline__ Plan plan_of(int rows, int cols) {
 __device__ __forceinline__ uint32_t group_address(uint32_t tile, uint32_t chunk_bytes, int row,
                                                   int col) {
   return chunk_address(tile + (uint32_t)(col >> 6) * chunk_bytes, row, (col >> 3) & 7);
+}
+
+__device__ __forceinline__ void store_half(uint32_t addr, float v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(__half_as_ushort(__float2half_rn(v)))
+               : "memory");
 }
 
 // SRC: 0 fp32 and 1 bf16 matrices to orthogonalize; 2 + type + 2 (4 bits) a step.
@@ -126,58 +131,83 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     const uint8_t* gm = static_cast<const uint8_t*>(grads) + mat * n * (T == kBf16 ? 2 : 4);
     const bool vec = aligned16(gm);
     const int64_t base = mat * Q.bpm;
+    // Chunks of kHeld blocks per half-warp; a matrix of one chunk stays in
+    // registers between the passes.
+    constexpr int kHeld = 3;
+    constexpr int kChunk = kHeld * (kThreads / 16);
+    float gv[kHeld][8], scale[kHeld];
+    uint2 codes[kHeld];
+    auto fetch = [&](int64_t b0) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const int64_t b = b0 + half + k * (kThreads / 16);
+        codes[k] = make_uint2(0u, 0u);
+        scale[k] = 0.0f;
+        if (b < Q.bpm) {
+          codes[k] = load_codes<BITS>(Q.codes, base + b, sub);
+          scale[k] = Q.scales[base + b];
+        }
+        load8<T>(gm, b * kMuonBlock + 8 * sub, n, vec, gv[k]);
+      }
+    };
     double sum = 0.0;
-    for (int64_t b = half; b < Q.bpm; b += kThreads / 16) {
-      float q[8], m[8], u[8], gv[8];
-      load8<T>(gm, b * kMuonBlock + 8 * sub, n, vec, gv);
-      unpack8<BITS>(load_codes<BITS>(Q.codes, base + b, sub), q);
-      new_momentum(q, Q.scales[base + b], gv, beta, nesterov, m, u);
-      sum += sum_squares(u);
+    for (int64_t b0 = 0; b0 < Q.bpm; b0 += kChunk) {
+      fetch(b0);
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        float q[8], m[8], u[8];
+        unpack8<BITS>(codes[k], q);
+        new_momentum(q, scale[k], gv[k], beta, nesterov, m, u);
+        sum += sum_squares(u);
+      }
     }
     sum = cta_sum<kThreads>(sum);
     if (threadIdx.x == 0) scale_s = scale_of(sum, eps, e0);
     __syncthreads();
     const NormScale ns = scale_s;
     bool bad = false;
-    for (int64_t b0 = 2 * warp; b0 < Q.bpm; b0 += kThreads / 16) {
-      const int64_t b = b0 + (half & 1);
-      const bool live = b < Q.bpm;
-      const int64_t i = b * kMuonBlock + 8 * sub;
-      float q[8], m[8], u[8], gv[8];
-      load8<T>(gm, i, n, vec, gv);
-      uint2 codes = make_uint2(0u, 0u);
-      float scale = 0.0f;
-      if (live) {
-        codes = load_codes<BITS>(Q.codes, base + b, sub);
-        scale = Q.scales[base + b];
-      }
-      unpack8<BITS>(codes, q);
-      new_momentum(q, scale, gv, beta, nesterov, m, u);
-      uint32_t c[8];
-      quantize_block<BITS>(m, i, n, (uint64_t)(rnd.base + (base + b) * kMuonBlock) / 8 + sub, rnd,
-                           scale, c, bad);
-      if (live) {
-        store_codes<BITS>(Q.codes, base + b, sub, c);
-        if (sub == 0) Q.scales[base + b] = scale;
-        int row = (int)((uint32_t)i / (uint32_t)sh.cols);
-        int col = (int)i - row * sh.cols;
+    for (int64_t b0 = 0; b0 < Q.bpm; b0 += kChunk) {
+      if (Q.bpm > kChunk) fetch(b0);
+#pragma unroll 1
+      for (int k = 0; k < kHeld; ++k) {
+        const int64_t b = b0 + half + k * (kThreads / 16);
+        if (b0 + 2 * warp + k * (kThreads / 16) >= Q.bpm) break;
+        const int64_t i = b * kMuonBlock + 8 * sub;
+        const int left = left_of(i, n);
+        float q[8], m[8], u[8], now[8], old_scale = 0.0f, new_scale;
+        uint2 old_codes = make_uint2(0u, 0u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = u[e] * ns.first * ns.second;
-        if ((sh.cols & 7) == 0) {  // eight values of one row
-          if (i < n)
-            st_shared(group_address(X, p.xs, row, col), pack_f16(u[0], u[1]),
-                      pack_f16(u[2], u[3]), pack_f16(u[4], u[5]), pack_f16(u[6], u[7]));
-        } else {
+        for (int h = 0; h < kHeld; ++h)
+          if (h == k) {
+            old_codes = codes[h];
+            old_scale = scale[h];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (i + e < n)
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(group_address(X, p.xs, row, col) +
-                                                           2u * (col & 7)),
-                           "h"(__half_as_ushort(__float2half_rn(u[e])))
-                           : "memory");
-            if (++col == sh.cols) {
-              col = 0;
-              ++row;
+            for (int e = 0; e < 8; ++e) now[e] = gv[h][e];
+          }
+        unpack8<BITS>(old_codes, q);
+        new_momentum(q, old_scale, now, beta, nesterov, m, u);
+        uint32_t c[8];
+        quantize_block<BITS>(m, left, (uint64_t)(rnd.base + (base + b) * kMuonBlock) / 8 + sub, rnd,
+                             new_scale, c, bad);
+        if (b < Q.bpm) {
+          store_codes<BITS>(Q.codes, base + b, sub, c);
+          if (sub == 0) Q.scales[base + b] = new_scale;
+          int row = (int)((uint32_t)i / (uint32_t)sh.cols);
+          int col = (int)i - row * sh.cols;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] = u[e] * ns.first * ns.second;
+          if ((sh.cols & 7) == 0) {  // eight values of one row
+            if (left > 0)
+              st_shared(group_address(X, p.xs, row, col), pack_f16(u[0], u[1]),
+                        pack_f16(u[2], u[3]), pack_f16(u[4], u[5]), pack_f16(u[6], u[7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if (e < left) store_half(group_address(X, p.xs, row, col) + 2u * (col & 7), u[e]);
+              if (++col == sh.cols) {
+                col = 0;
+                ++row;
+              }
             }
           }
         }
@@ -199,20 +229,20 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
   volatile uint32_t* stop_v = &stop;
   uint32_t turn = 0;
   bool ok = true;
-  // Waits for the MMAs issued; false (in every thread) when the CTA gives up.
+  // Waits for the MMAs issued. A thread that gives up goes on to the next
+  // publish(), where the CTA stops as one; what it reads until then is unused.
   auto finish = [&]() {
-    const bool mine = mbar_wait(smem_u32(&done), turn, g.wait_ns, stop_v);
-    ok = __syncthreads_or(!mine) == 0;
+    ok = mbar_wait(smem_u32(&done), turn, g.wait_ns, stop_v);
     fence_after();
-    if (ok) turn ^= 1u;
-    return ok;
   };
   // Every thread's tile writes and TMEM reads come before the next MMAs.
   auto publish = [&]() {
     fence_async_shared();
     fence_before();
-    __syncthreads();
+    ok = __syncthreads_or(!ok) == 0;
     fence_after();
+    if (ok) turn ^= 1u;
+    return ok;
   };
 
   for (int k = 0; ok && k < g.steps; ++k) {
@@ -235,7 +265,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
       mma_commit<1>(smem_u32(&done));
     }
     __syncwarp();
-    if (!finish()) break;
+    finish();
     if (quarter * 32 < p.s16) {
       const float alpha = k == 0 ? g.gram_alpha[0] * factor * factor : g.gram_alpha[k];
       for (int u = part; u < sunits; u += 4) {
@@ -256,7 +286,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
         __syncwarp();
       }
     }
-    publish();
+    if (!publish()) break;
 
     // P = a I + b A + c A A
     if (warp == 0 && elect_one()) {
@@ -268,7 +298,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
       mma_commit<1>(smem_u32(&done));
     }
     __syncwarp();
-    if (!finish()) break;
+    finish();
     if (quarter * 32 < p.s16) {
       const float alpha = g.poly_alpha[k], mid = g.poly_mid[k], diag = g.poly_diag[k];
       for (int u = part; u < sunits; u += 4) {
@@ -297,50 +327,41 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
         __syncwarp();
       }
     }
-    publish();
+    if (!publish()) break;
 
-    // X' = f P X (X P), 512 accumulator columns at a time; a pass replaces only
-    // the columns (rows) of X that no other pass reads.
+    // X' = f P X (X P), with the long side along the accumulator rows either
+    // way so that all TMEM lanes work: tile t holds its rows 128 t .. in columns
+    // s16 t .. of a pass of up to 512 columns. A pass replaces only what no
+    // other tile reads.
     const bool last = k == g.steps - 1;
     const float alpha = k == 0 ? g.update_alpha[0] * factor : g.update_alpha[k];
-    const int tiles = p.tall ? (p.l + 127) / 128 : 1;
-    const int pass = p.tall ? 512 / p.s16 : 512;      // tiles, or columns
-    const int total = p.tall ? tiles : p.l16;
-    for (int p0 = 0; p0 < total; p0 += pass) {
-      const int now = min(pass, total - p0);
+    const int tiles = (p.l + 127) / 128, pass = 512 / p.s16;
+    for (int p0 = 0; ok && p0 < tiles; p0 += pass) {
+      const int now = min(pass, tiles - p0);
       if (warp == 0 && elect_one()) {
-        if (p.tall) {
-          const uint32_t idesc = instruction_desc<1>(p.s16, false, false);
-          for (int t = 0; t < now; ++t)
-            for (int kk = 0; kk < sunits; ++kk)
-              mma_f16<1>(tmem + t * p.s16,
-                         operand_desc(X + (kk >> 2) * p.xs + (p0 + t) * 16384 + (kk & 3) * 32, 16),
-                         operand_desc(P + (kk >> 2) * p.ps + (kk & 3) * 32, 16), idesc, kk != 0);
-        } else {
-          for (int n0 = 0; n0 < now; n0 += 256) {
-            const uint32_t idesc = instruction_desc<1>(min(256, now - n0), false, true);
-            for (int kk = 0; kk < sunits; ++kk)
-              mma_f16<1>(tmem + n0, operand_desc(P + (kk >> 2) * p.ps + (kk & 3) * 32, 16),
-                         operand_desc(X + ((p0 + n0) >> 6) * p.xs + kk * 2048, p.xs), idesc,
-                         kk != 0);
+        const uint32_t idesc = instruction_desc<1>(p.s16, !p.tall, false);
+        for (int t = 0; t < now; ++t)
+          for (int kk = 0; kk < sunits; ++kk) {
+            const uint64_t a =
+                p.tall ? operand_desc(X + (kk >> 2) * p.xs + (p0 + t) * 16384 + (kk & 3) * 32, 16)
+                       : operand_desc(X + 2 * (p0 + t) * p.xs + kk * 2048, p.xs);
+            mma_f16<1>(tmem + t * p.s16, a,
+                       operand_desc(P + (kk >> 2) * p.ps + (kk & 3) * 32, 16), idesc, kk != 0);
           }
-        }
         mma_commit<1>(smem_u32(&done));
       }
       __syncwarp();
-      if (!finish()) break;
-      const int units = p.tall ? now * sunits : now / 16;
-      for (int u = part; u < units; u += 4) {
-        const int t = p.tall ? u / sunits : 0;
-        const int row0 = p.tall ? (p0 + t) * 128 + quarter * 32 : quarter * 32;
-        const int col = p.tall ? 16 * (u - t * sunits) : p0 + 16 * u;
-        if (row0 >= (p.tall ? p.l16 : p.s16)) continue;
+      finish();
+      for (int u = part; u < now * sunits; u += 4) {
+        const int t = u / sunits, j0 = 16 * (u - t * sunits);  // short side j0 .. j0 + 15
+        const int i0 = (p0 + t) * 128 + quarter * 32;          // long side
+        if (i0 >= p.l16) continue;
         uint32_t v[16];
         tmem_load16(lanes + 16 * u, v);
         tmem_load_wait();
-        const int row = row0 + lane;
-        if (!last) {
-          if (row < (p.tall ? p.l16 : p.s16)) {
+        const int i = i0 + lane;
+        if (!last && p.tall) {
+          if (i < p.l16) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t w[4];
@@ -348,22 +369,42 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
               for (int e = 0; e < 4; ++e)
                 w[e] = pack_f16(__uint_as_float(v[8 * h + 2 * e]) * alpha,
                                 __uint_as_float(v[8 * h + 2 * e + 1]) * alpha);
-              st_shared(group_address(X, p.xs, row, col + 8 * h), w[0], w[1], w[2], w[3]);
+              st_shared(group_address(X, p.xs, i, j0 + 8 * h), w[0], w[1], w[2], w[3]);
             }
           }
-        } else if (row < sh.rows) {
+        } else if (!last) {
+          // A lane's value of 16 rows: 32 lanes write 64 contiguous bytes of each.
+          if (i < p.l16) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const float y[4] = {__uint_as_float(v[4 * h]), __uint_as_float(v[4 * h + 1]),
-                                __uint_as_float(v[4 * h + 2]), __uint_as_float(v[4 * h + 3])};
-            if (col + 4 * h < sh.cols)
-              write_out(g, mat * g.batch_stride + (int64_t)row * g.ldo + col + 4 * h,
-                        sh.cols - col - 4 * h, y, alpha);
+            for (int e = 0; e < 16; ++e)
+              store_half(group_address(X, p.xs, j0 + e, i) + 2u * (i & 7),
+                         __uint_as_float(v[e]) * alpha);
+          }
+        } else if (i < p.l) {
+          const int64_t at = mat * g.batch_stride + (p.tall ? i * g.ldo + j0 : j0 * g.ldo + i);
+          if (p.tall) {
+            float4 old[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) old[h] = read_four(g, at + 4 * h, p.s - j0 - 4 * h);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const uint32_t y[4] = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+              if (j0 + 4 * h < p.s) write_four(g, at + 4 * h, p.s - j0 - 4 * h, old[h], y, alpha);
+            }
+          } else {
+            float old[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              old[e] = j0 + e < p.s ? read_one(g, at + e * g.ldo) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (j0 + e < p.s)
+                write_one(g, at + e * g.ldo, new_value(g, old[e], __uint_as_float(v[e]), alpha));
           }
         }
         __syncwarp();
       }
-      publish();
+      if (!publish()) break;
     }
   }
   // MMAs in flight end before shared memory and TMEM go.

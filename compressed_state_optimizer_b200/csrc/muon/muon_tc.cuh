@@ -239,54 +239,60 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t a) {
   return v;
 }
 
-// Four consecutive columns of a caller's row: the result, or the parameters'
-// update formed in fp32 and rounded once.
-__device__ __forceinline__ void write_out(const MuonNs& g, int64_t at, int left, const float (&x)[4],
-                                          float alpha) {
-  if (g.params) {
+// One value of the last product: the result, or a parameter's update formed in
+// fp32 and rounded once.
+__device__ __forceinline__ float new_value(const MuonNs& g, float old, float x, float alpha) {
+  return g.params ? fmaf(-alpha, x, old * g.decay) : x * alpha;
+}
+__device__ __forceinline__ float read_one(const MuonNs& g, int64_t at) {
+  if (!g.params) return 0.0f;
+  if (g.out_type == kF32) return static_cast<const float*>(g.out)[at];
+  return __uint_as_float((uint32_t)static_cast<const uint16_t*>(g.out)[at] << 16);
+}
+__device__ __forceinline__ void write_one(const MuonNs& g, int64_t at, float v) {
+  if (g.out_type == kF32)
+    static_cast<float*>(g.out)[at] = v;
+  else
+    static_cast<uint16_t*>(g.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+// Four consecutive columns of a row, `left` of them inside it.
+__device__ __forceinline__ float4 read_four(const MuonNs& g, int64_t at, int left) {
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (!g.params) return v;
+  if (g.out_vec && left >= 4) {
     if (g.out_type == kF32) {
-      float* p = static_cast<float*>(g.out) + at;
-      if (g.out_vec && left >= 4) {
-        float4 v = *reinterpret_cast<const float4*>(p);
-        v.x = fmaf(-alpha, x[0], v.x * g.decay);
-        v.y = fmaf(-alpha, x[1], v.y * g.decay);
-        v.z = fmaf(-alpha, x[2], v.z * g.decay);
-        v.w = fmaf(-alpha, x[3], v.w * g.decay);
-        *reinterpret_cast<float4*>(p) = v;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < left) p[e] = fmaf(-alpha, x[e], p[e] * g.decay);
-      }
+      v = *reinterpret_cast<const float4*>(static_cast<const float*>(g.out) + at);
     } else {
-      uint16_t* p = static_cast<uint16_t*>(g.out) + at;
-      if (g.out_vec && left >= 4) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        const float a0 = __uint_as_float(v.x << 16), a1 = __uint_as_float(v.x & 0xFFFF0000u);
-        const float a2 = __uint_as_float(v.y << 16), a3 = __uint_as_float(v.y & 0xFFFF0000u);
-        *reinterpret_cast<uint2*>(p) =
-            make_uint2(pack_bf16(fmaf(-alpha, x[0], a0 * g.decay), fmaf(-alpha, x[1], a1 * g.decay)),
-                       pack_bf16(fmaf(-alpha, x[2], a2 * g.decay), fmaf(-alpha, x[3], a3 * g.decay)));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < left) {
-            const float v = __uint_as_float((uint32_t)p[e] << 16);
-            p[e] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(-alpha, x[e], v * g.decay)));
-          }
-      }
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g.out) + at);
+      v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
     }
-  } else {
-    uint16_t* p = static_cast<uint16_t*>(g.out) + at;
-    if (g.out_vec && left >= 4) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0] * alpha, x[1] * alpha),
-                                                pack_bf16(x[2] * alpha, x[3] * alpha));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < left) p[e] = __bfloat16_as_ushort(__float2bfloat16_rn(x[e] * alpha));
-    }
+    return v;
   }
+  if (left > 0) v.x = read_one(g, at);
+  if (left > 1) v.y = read_one(g, at + 1);
+  if (left > 2) v.z = read_one(g, at + 2);
+  if (left > 3) v.w = read_one(g, at + 3);
+  return v;
+}
+__device__ __forceinline__ void write_four(const MuonNs& g, int64_t at, int left, float4 old,
+                                           const uint32_t (&x)[4], float alpha) {
+  const float v[4] = {new_value(g, old.x, __uint_as_float(x[0]), alpha),
+                      new_value(g, old.y, __uint_as_float(x[1]), alpha),
+                      new_value(g, old.z, __uint_as_float(x[2]), alpha),
+                      new_value(g, old.w, __uint_as_float(x[3]), alpha)};
+  if (g.out_vec && left >= 4) {
+    if (g.out_type == kF32)
+      *reinterpret_cast<float4*>(static_cast<float*>(g.out) + at) =
+          make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + at) =
+          make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) write_one(g, at + e, v[e]);
 }
 
 }  // namespace
