@@ -129,15 +129,16 @@ __device__ __forceinline__ bool reads_mn(const MuonNs& g, int kind, bool a, int 
 __device__ __forceinline__ bool matrix_wait(const MuonNs& g, int z, uint32_t want,
                                             volatile uint32_t* stop) {
   const uint32_t* p = g.counters + z;
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  if (v >= want) return true;
-  const uint64_t t0 = now_ns();
-  while (true) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    uint32_t v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     if (v >= want) return true;
+    if (g.wait_ns != 0 && (n & 63u) != 0) continue;
     if (*stop) return false;
-    if (g.wait_ns == 0 || now_ns() - t0 > g.wait_ns) {
+    const uint64_t t = now_ns();
+    if (t0 == 0) t0 = t;
+    if (g.wait_ns == 0 || t - t0 > g.wait_ns) {
       *stop = 1;
       return false;
     }

@@ -223,10 +223,12 @@ __device__ __forceinline__ double cta_sum(double v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = v;
   __syncthreads();
-  double s = 0.0;
-  if (threadIdx.x == 0)
-    for (int w = 0; w < T / 32; ++w) s += warp_sums[w];
-  return s;
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < T / 32 ? warp_sums[threadIdx.x] : 0.0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  }
+  return v;
 }
 
 // 2^(e0 - t) as two factors (each an fp32 power of two) and 2^t / (|x| + eps),

@@ -3,8 +3,8 @@
 // MMAs read (128-byte swizzled rows of 64 elements), accumulators in TMEM;
 // global memory is read once or twice at the start and written once at the end.
 //
-// Each of the 3 products per step is a handful of MMAs followed by an epilogue
-// of all 16 warps, so a step is bound by the latency of issue, completion,
+// Each of the 3 products per step is a handful of MMAs, issued by a warp of
+// their own, followed by an epilogue of the 16 others, so a step is bound by the latency of issue, completion,
 // TMEM read and CTA barrier, not by arithmetic. X has the caller's orientation
 // (s = short, l = long side): a wide one is s rows of ceil(l / 64) chunks, a
 // tall one l rows of ceil(s / 64) chunks, rows and contracted columns padded
@@ -18,7 +18,8 @@
 namespace mua {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kWorkers = 512;             // warps 0 .. 15; warp 16 issues the MMAs
+constexpr int kThreads = kWorkers + 32;
 constexpr uint32_t kOverread = 16384;  // 128 rows of a chunk that starts at its last row
 
 __host__ __device__ __forceinline__ int round16(int x) { return (x + 15) & ~15; }
@@ -63,6 +64,53 @@ __device__ __forceinline__ void store_half(uint32_t addr, float v) {
                : "memory");
 }
 
+// The last product's 16 values of a lane, `left` of them inside the matrix, in
+// one row at `at` (four columns a time) or one column (32 lanes are 32
+// neighbouring columns). All loads come before the first store.
+__device__ __forceinline__ void finish_columns(const MuonNs& g, uint32_t tmem, int64_t at, int left,
+                                               float alpha) {
+  float4 old[4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) old[h] = read_four(g, at + 4 * h, left - 4 * h);
+  uint32_t v[16];
+  tmem_load16(tmem, v);
+  tmem_load_wait();
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const uint32_t y[4] = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+    if (4 * h < left) write_four(g, at + 4 * h, left - 4 * h, old[h], y, alpha);
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void finish_rows(const MuonNs& g, uint32_t tmem, int64_t at, int left,
+                                            float alpha) {
+  float old[16];
+  uint32_t v[16];
+  if (g.out_type == kF32) {
+    float* p = static_cast<float*>(g.out) + at;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) old[e] = e < left ? p[e * g.ldo] : 0.0f;
+    tmem_load16(tmem, v);
+    tmem_load_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (e < left) p[e * g.ldo] = new_value(g, old[e], __uint_as_float(v[e]), alpha);
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(g.out) + at;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      old[e] = g.params && e < left ? __uint_as_float((uint32_t)p[e * g.ldo] << 16) : 0.0f;
+    tmem_load16(tmem, v);
+    tmem_load_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (e < left)
+        p[e * g.ldo] = __bfloat16_as_ushort(
+            __float2bfloat16_rn(new_value(g, old[e], __uint_as_float(v[e]), alpha)));
+  }
+  __syncwarp();
+}
+
 // SRC: 0 fp32 and 1 bf16 matrices to orthogonalize; 2 + type + 2 (4 bits) a step.
 template <int SRC>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -88,7 +136,8 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) {
+  const bool worker = warp < kWorkers / 32;
+  if (!worker) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&tmem_base_s)),
                  "r"(p.columns)
@@ -97,7 +146,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
   }
   // Rows and columns that pad a side to 16 hold zeros throughout.
   if (((p.s | p.l) & 15) != 0)
-    for (uint32_t o = threadIdx.x * 16; o < p.a_off; o += kThreads * 16)
+    for (uint32_t o = threadIdx.x * 16; worker && o < p.a_off; o += kWorkers * 16)
       st_shared(X + o, 0u, 0u, 0u, 0u);
 
   // The norm, then X_0 = x 2^(e0 - t): see muon_launch_load.
@@ -107,20 +156,34 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     const bool vec = aligned16(xm) && (x.row_stride * es) % 16 == 0;
     const uint32_t per_row = (uint32_t)(sh.cols + 7) / 8, groups = per_row * (uint32_t)sh.rows;
     double sum = 0.0;
-    for (uint32_t q = threadIdx.x; q < groups; q += kThreads) {
-      const uint32_t row = q / per_row, col = 8 * (q - row * per_row);
-      float v[8];
-      load8<T>(xm + (int64_t)row * x.row_stride * es, col, sh.cols, vec, v);
-      sum += sum_squares(v);
+    // Up to kHeld groups of 8 per thread stay in registers between the passes.
+    constexpr int kHeld = 2;
+    float held[kHeld][8];
+    for (uint32_t q0 = threadIdx.x; worker && q0 < groups; q0 += kHeld * kWorkers) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const uint32_t q = q0 + k * kWorkers;
+        const uint32_t row = q / per_row, col = 8 * (q - row * per_row);
+        const int64_t end = q < groups ? sh.cols : 0;
+        load8<T>(xm + (int64_t)row * x.row_stride * es, col, end, vec, held[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) sum += sum_squares(held[k]);
     }
     sum = cta_sum<kThreads>(sum);
     if (threadIdx.x == 0) scale_s = scale_of(sum, eps, e0);
     __syncthreads();
     const NormScale ns = scale_s;
-    for (uint32_t q = threadIdx.x; q < groups; q += kThreads) {
+#pragma unroll 1
+    for (uint32_t q = threadIdx.x, k = 0; worker && q < groups; q += kWorkers, ++k) {
       const uint32_t row = q / per_row, col = 8 * (q - row * per_row);
       float v[8];
-      load8<T>(xm + (int64_t)row * x.row_stride * es, col, sh.cols, vec, v);
+      if (groups > kHeld * kWorkers) {
+        load8<T>(xm + (int64_t)row * x.row_stride * es, col, sh.cols, vec, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = k == 0 ? held[0][e] : held[1][e];
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = v[e] * ns.first * ns.second;
       st_shared(group_address(X, p.xs, (int)row, (int)col), pack_f16(v[0], v[1]),
@@ -134,13 +197,13 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     // Chunks of kHeld blocks per half-warp; a matrix of one chunk stays in
     // registers between the passes.
     constexpr int kHeld = 3;
-    constexpr int kChunk = kHeld * (kThreads / 16);
+    constexpr int kChunk = kHeld * (kWorkers / 16);
     float gv[kHeld][8], scale[kHeld];
     uint2 codes[kHeld];
     auto fetch = [&](int64_t b0) {
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
-        const int64_t b = b0 + half + k * (kThreads / 16);
+        const int64_t b = b0 + half + k * (kWorkers / 16);
         codes[k] = make_uint2(0u, 0u);
         scale[k] = 0.0f;
         if (b < Q.bpm) {
@@ -151,7 +214,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
       }
     };
     double sum = 0.0;
-    for (int64_t b0 = 0; b0 < Q.bpm; b0 += kChunk) {
+    for (int64_t b0 = 0; worker && b0 < Q.bpm; b0 += kChunk) {
       fetch(b0);
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
@@ -166,12 +229,12 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     __syncthreads();
     const NormScale ns = scale_s;
     bool bad = false;
-    for (int64_t b0 = 0; b0 < Q.bpm; b0 += kChunk) {
+    for (int64_t b0 = 0; worker && b0 < Q.bpm; b0 += kChunk) {
       if (Q.bpm > kChunk) fetch(b0);
 #pragma unroll 1
       for (int k = 0; k < kHeld; ++k) {
-        const int64_t b = b0 + half + k * (kThreads / 16);
-        if (b0 + 2 * warp + k * (kThreads / 16) >= Q.bpm) break;
+        const int64_t b = b0 + half + k * (kWorkers / 16);
+        if (b0 + 2 * warp + k * (kWorkers / 16) >= Q.bpm) break;
         const int64_t i = b * kMuonBlock + 8 * sub;
         const int left = left_of(i, n);
         float q[8], m[8], u[8], now[8], old_scale = 0.0f, new_scale;
@@ -245,86 +308,97 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     return ok;
   };
 
+  // The issuing warp runs converged (descriptors stay in uniform registers).
+  const uint32_t sym_idesc = instruction_desc<1>(p.s16, false, false);
   for (int k = 0; ok && k < g.steps; ++k) {
     // A = f^2 X X^T
-    if (warp == 0 && elect_one()) {
-      const uint32_t idesc = instruction_desc<1>(p.s16, p.tall, p.tall);
+    if (!worker) {
+      const bool lead = elect_one();
       if (p.tall) {
+        const uint32_t idesc = instruction_desc<1>(p.s16, true, true);
         // 64 further rows of A behind a single chunk: the chunk again.
-        const uint32_t lead = p.ns > 1 ? p.xs : 0;
-        for (int kk = 0; kk < p.l16 / 16; ++kk) {
-          const uint64_t d = operand_desc(X + kk * 2048, lead);
-          mma_f16<1>(tmem, d, d, idesc, kk != 0);
-        }
+        uint64_t d = operand_desc(X, p.ns > 1 ? p.xs : 0);
+        for (int kk = 0; kk < p.l16 / 16; ++kk, d += 2048 >> 4)
+          if (lead) mma_f16<1>(tmem, d, d, idesc, kk != 0);
       } else {
-        for (int kk = 0; kk < p.l16 / 16; ++kk) {
-          const uint64_t d = operand_desc(X + (kk >> 2) * p.xs + (kk & 3) * 32, 16);
-          mma_f16<1>(tmem, d, d, idesc, kk != 0);
+        uint64_t chunk = operand_desc(X, 16);
+        for (int left = p.l16 / 16, first = 1; left > 0; left -= 4, chunk += p.xs >> 4) {
+          uint64_t d = chunk;
+          for (int kk = 0; kk < min(4, left); ++kk, d += 32 >> 4, first = 0)
+            if (lead) mma_f16<1>(tmem, d, d, sym_idesc, first == 0);
         }
       }
-      mma_commit<1>(smem_u32(&done));
+      if (lead) mma_commit<1>(smem_u32(&done));
+      __syncwarp();
     }
-    __syncwarp();
     finish();
-    if (quarter * 32 < p.s16) {
+    uint32_t held[2][8];  // this thread's part of A, for the next product
+    if (worker && quarter * 32 < p.s16) {
       const float alpha = k == 0 ? g.gram_alpha[0] * factor * factor : g.gram_alpha[k];
-      for (int u = part; u < sunits; u += 4) {
-        uint32_t v[16];
-        tmem_load16(lanes + 16 * u, v);
-        tmem_load_wait();
-        if (lane_row < p.s16) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w[4];
+      for (int q = 0; q < 2; ++q) {
+        const int u = part + 4 * q;
+        if (u < sunits) {
+          uint32_t v[16];
+          tmem_load16(lanes + 16 * u, v);
+          tmem_load_wait();
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_f16(__uint_as_float(v[8 * h + 2 * e]) * alpha,
-                              __uint_as_float(v[8 * h + 2 * e + 1]) * alpha);
-            st_shared(group_address(A, p.ps, lane_row, 16 * u + 8 * h), w[0], w[1], w[2], w[3]);
+          for (int e = 0; e < 8; ++e)
+            held[q][e] = pack_f16(__uint_as_float(v[2 * e]) * alpha,
+                                  __uint_as_float(v[2 * e + 1]) * alpha);
+          if (lane_row < p.s16) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              st_shared(group_address(A, p.ps, lane_row, 16 * u + 8 * h), held[q][4 * h],
+                        held[q][4 * h + 1], held[q][4 * h + 2], held[q][4 * h + 3]);
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
     if (!publish()) break;
 
     // P = a I + b A + c A A
-    if (warp == 0 && elect_one()) {
-      const uint32_t idesc = instruction_desc<1>(p.s16, false, false);
-      for (int kk = 0; kk < sunits; ++kk) {
-        const uint64_t d = operand_desc(A + (kk >> 2) * p.ps + (kk & 3) * 32, 16);
-        mma_f16<1>(tmem, d, d, idesc, kk != 0);
+    if (!worker) {
+      const bool lead = elect_one();
+      uint64_t chunk = operand_desc(A, 16);
+      for (int left = sunits, first = 1; left > 0; left -= 4, chunk += p.ps >> 4) {
+        uint64_t d = chunk;
+        for (int kk = 0; kk < min(4, left); ++kk, d += 32 >> 4, first = 0)
+          if (lead) mma_f16<1>(tmem, d, d, sym_idesc, first == 0);
       }
-      mma_commit<1>(smem_u32(&done));
+      if (lead) mma_commit<1>(smem_u32(&done));
+      __syncwarp();
     }
-    __syncwarp();
     finish();
-    if (quarter * 32 < p.s16) {
+    if (worker && quarter * 32 < p.s16) {
       const float alpha = g.poly_alpha[k], mid = g.poly_mid[k], diag = g.poly_diag[k];
-      for (int u = part; u < sunits; u += 4) {
-        uint32_t v[16];
-        tmem_load16(lanes + 16 * u, v);
-        tmem_load_wait();
-        if (lane_row < p.s16) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int col = 16 * u + 8 * h;
-            const uint4 a = ld_shared(group_address(A, p.ps, lane_row, col));
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-            uint32_t w[4];
+      for (int q = 0; q < 2; ++q) {
+        const int u = part + 4 * q;
+        if (u < sunits) {
+          uint32_t v[16];
+          tmem_load16(lanes + 16 * u, v);
+          tmem_load_wait();
+          const int diagonal = lane_row < p.s ? lane_row - 16 * u : -1;
+          uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
-              float x0 = fmaf(y.x, mid, __uint_as_float(v[8 * h + 2 * e]) * alpha);
-              float x1 = fmaf(y.y, mid, __uint_as_float(v[8 * h + 2 * e + 1]) * alpha);
-              if (col + 2 * e == lane_row && lane_row < p.s) x0 += diag;
-              if (col + 2 * e + 1 == lane_row && lane_row < p.s) x1 += diag;
-              w[e] = pack_f16(x0, x1);
-            }
-            st_shared(group_address(P, p.ps, lane_row, col), w[0], w[1], w[2], w[3]);
+          for (int e = 0; e < 8; ++e) {
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&held[q][e]));
+            float x0 = fmaf(y.x, mid, __uint_as_float(v[2 * e]) * alpha);
+            float x1 = fmaf(y.y, mid, __uint_as_float(v[2 * e + 1]) * alpha);
+            if (2 * e == diagonal) x0 += diag;
+            if (2 * e + 1 == diagonal) x1 += diag;
+            w[e] = pack_f16(x0, x1);
           }
+          if (lane_row < p.s16) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              st_shared(group_address(P, p.ps, lane_row, 16 * u + 8 * h), w[4 * h], w[4 * h + 1],
+                        w[4 * h + 2], w[4 * h + 3]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
     if (!publish()) break;
@@ -338,69 +412,67 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     const int tiles = (p.l + 127) / 128, pass = 512 / p.s16;
     for (int p0 = 0; ok && p0 < tiles; p0 += pass) {
       const int now = min(pass, tiles - p0);
-      if (warp == 0 && elect_one()) {
+      if (!worker) {
+        const bool lead = elect_one();
         const uint32_t idesc = instruction_desc<1>(p.s16, !p.tall, false);
-        for (int t = 0; t < now; ++t)
-          for (int kk = 0; kk < sunits; ++kk) {
-            const uint64_t a =
-                p.tall ? operand_desc(X + (kk >> 2) * p.xs + (p0 + t) * 16384 + (kk & 3) * 32, 16)
-                       : operand_desc(X + 2 * (p0 + t) * p.xs + kk * 2048, p.xs);
-            mma_f16<1>(tmem + t * p.s16, a,
-                       operand_desc(P + (kk >> 2) * p.ps + (kk & 3) * 32, 16), idesc, kk != 0);
+        // Tall: rows of X, 16 columns a step, 64 a chunk. Wide: columns of X (two
+        // chunks a tile), 16 rows a step.
+        uint64_t tile = p.tall ? operand_desc(X + p0 * 16384, 16)
+                               : operand_desc(X + 2 * p0 * p.xs, p.xs);
+        const uint64_t tile_step = p.tall ? 16384 >> 4 : (2 * p.xs) >> 4;
+        const uint64_t a_step = p.tall ? 32 >> 4 : 2048 >> 4;
+        const uint64_t a_chunk = p.tall ? p.xs >> 4 : 4 * (2048 >> 4);
+        const uint64_t b0 = operand_desc(P, 16);
+        for (int t = 0; t < now; ++t, tile += tile_step) {
+          uint64_t a_at = tile, b_at = b0;
+          for (int left = sunits, first = 1; left > 0;
+               left -= 4, a_at += a_chunk, b_at += p.ps >> 4) {
+            uint64_t a = a_at, b = b_at;
+            for (int kk = 0; kk < min(4, left); ++kk, a += a_step, b += 32 >> 4, first = 0)
+              if (lead) mma_f16<1>(tmem + t * p.s16, a, b, idesc, first == 0);
           }
-        mma_commit<1>(smem_u32(&done));
+        }
+        if (lead) mma_commit<1>(smem_u32(&done));
+        __syncwarp();
       }
-      __syncwarp();
       finish();
-      for (int u = part; u < now * sunits; u += 4) {
+      for (int u = part; worker && u < now * sunits; u += 4) {
         const int t = u / sunits, j0 = 16 * (u - t * sunits);  // short side j0 .. j0 + 15
         const int i0 = (p0 + t) * 128 + quarter * 32;          // long side
         if (i0 >= p.l16) continue;
-        uint32_t v[16];
+        const int i = i0 + lane;
+        if (last) {
+          const int64_t at = mat * g.batch_stride + (p.tall ? i * g.ldo + j0 : j0 * g.ldo + i);
+          if (p.tall)
+            finish_columns(g, lanes + 16 * u, at, i < p.l ? p.s - j0 : 0, alpha);
+          else
+            finish_rows(g, lanes + 16 * u, at, i < p.l ? p.s - j0 : 0, alpha);
+          continue;
+        }
+        uint32_t v[16], w[8];
         tmem_load16(lanes + 16 * u, v);
         tmem_load_wait();
-        const int i = i0 + lane;
-        if (!last && p.tall) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          w[e] = pack_f16(__uint_as_float(v[2 * e]) * alpha, __uint_as_float(v[2 * e + 1]) * alpha);
+        if (p.tall) {
           if (i < p.l16) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_f16(__uint_as_float(v[8 * h + 2 * e]) * alpha,
-                                __uint_as_float(v[8 * h + 2 * e + 1]) * alpha);
-              st_shared(group_address(X, p.xs, i, j0 + 8 * h), w[0], w[1], w[2], w[3]);
-            }
+            for (int h = 0; h < 2; ++h)
+              st_shared(group_address(X, p.xs, i, j0 + 8 * h), w[4 * h], w[4 * h + 1],
+                        w[4 * h + 2], w[4 * h + 3]);
           }
-        } else if (!last) {
+        } else if (i < p.l16) {
           // A lane's value of 16 rows: 32 lanes write 64 contiguous bytes of each.
-          if (i < p.l16) {
+          // Rows j0 + e, with j0 a multiple of 16, swizzle by e & 7.
+          const uint32_t base = X + (uint32_t)(i >> 6) * p.xs + j0 * 128 + 2 * (i & 7);
+          const uint32_t group = (uint32_t)(i & 56) << 1;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              store_half(group_address(X, p.xs, j0 + e, i) + 2u * (i & 7),
-                         __uint_as_float(v[e]) * alpha);
-          }
-        } else if (i < p.l) {
-          const int64_t at = mat * g.batch_stride + (p.tall ? i * g.ldo + j0 : j0 * g.ldo + i);
-          if (p.tall) {
-            float4 old[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) old[h] = read_four(g, at + 4 * h, p.s - j0 - 4 * h);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const uint32_t y[4] = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
-              if (j0 + 4 * h < p.s) write_four(g, at + 4 * h, p.s - j0 - 4 * h, old[h], y, alpha);
-            }
-          } else {
-            float old[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              old[e] = j0 + e < p.s ? read_one(g, at + e * g.ldo) : 0.0f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (j0 + e < p.s)
-                write_one(g, at + e * g.ldo, new_value(g, old[e], __uint_as_float(v[e]), alpha));
-          }
+          for (int e = 0; e < 16; ++e)
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(base + e * 128 +
+                                                         (group ^ ((e & 7) << 4))),
+                         "h"((uint16_t)(w[e >> 1] >> (16 * (e & 1))))
+                         : "memory");
         }
         __syncwarp();
       }
@@ -410,7 +482,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
   // MMAs in flight end before shared memory and TMEM go.
   if (!ok) mbar_drain(smem_u32(&done), turn);
   __syncthreads();
-  if (warp == 0)
+  if (!worker)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(p.columns));
   if (threadIdx.x == 0 && stop) atomicOr(g.status, kMuonTimeout);

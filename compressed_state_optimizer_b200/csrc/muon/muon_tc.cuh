@@ -49,18 +49,18 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// False when the wait ran out, or another role of the CTA has given up.
-// A limit of 0 gives up as soon as it would wait.
+// False when the wait ran out, or another role of the CTA has given up. The
+// timer is read once in 1024 tries: a read takes longer than most waits. A
+// limit of 0 gives up as soon as it would wait.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit,
                                           volatile uint32_t* stop) {
-  for (int spin = 0; spin < 64; ++spin) {
-    if (mbar_try(bar, parity)) return true;
-    if (limit == 0) break;
-  }
-  const uint64_t t0 = now_ns();
-  while (limit == 0 || !mbar_try(bar, parity)) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try(bar, parity); ++n) {
+    if (limit != 0 && (n & 1023u) != 0) continue;
     if (*stop) return false;
-    if (limit == 0 || now_ns() - t0 > limit) {
+    const uint64_t t = now_ns();
+    if (t0 == 0) t0 = t;
+    if (limit == 0 || t - t0 > limit) {
       *stop = 1;
       return false;
     }
@@ -69,9 +69,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
 }
 // A wait for work in flight that other roles' giving up does not end.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-  if (mbar_try(bar, parity)) return;
-  const uint64_t t0 = now_ns();
-  while (!mbar_try(bar, parity) && now_ns() - t0 <= kDrainNs) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try(bar, parity); ++n) {
+    if ((n & 1023u) != 0) continue;
+    const uint64_t t = now_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kDrainNs) return;
   }
 }
 // A 64 x `rows` box into this CTA's shared memory. With CG = 2 the barrier may
