@@ -12,6 +12,7 @@ namespace mua {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kNormUnroll = 4;
 constexpr int kUnroll = 2;                             // blocks per half-warp
 constexpr int kChunkBlocks = kThreads / 16 * kUnroll;  // 32 blocks (4096 values) per CTA
 
@@ -27,7 +28,7 @@ __device__ __forceinline__ void release_next() {
 // Grid: splits x count CTAs, a CTA takes 32 consecutive blocks of one matrix.
 // OUT: 0 fp32, 1 bf16 (contiguous), 2 fp16 X_0 with row stride ld.
 template <int BITS, int G, int OUT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nesterov,
                 const __grid_constant__ MuonRandom rnd, void* out, const double* partials,
                 float eps, int e0, void* X, float* factor, uint32_t* counters, int splits) {
@@ -42,7 +43,7 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
   const int64_t first = (int64_t)split * kChunkBlocks + half;
   const int64_t base = mat * Q.bpm;
 
-  float gv[kUnroll][8];
+  uint64_t gv[kUnroll][4];
   uint2 codes[kUnroll];
   float scale[kUnroll];
 #pragma unroll
@@ -68,33 +69,36 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
 #pragma unroll
   for (int k = 0; k < kUnroll; ++k) {
     const int64_t b = first + k * (kThreads / 16);
-    float q[8], m[8], u[8];
+    uint64_t q[4], m[4], u[4];
     unpack8<BITS>(codes[k], q);
     new_momentum(q, scale[k], gv[k], beta, nesterov, m, u);
     const int64_t i = b * kMuonBlock + 8 * sub;
+    const int left = left_of(i, n);
     float new_scale;
     uint32_t c[8];
-    quantize_block<BITS>(m, left_of(i, n), (uint64_t)(rnd.base + (base + b) * kMuonBlock) / 8 + sub, rnd,
+    quantize_block<BITS>(m, left, (uint64_t)(rnd.base + (base + b) * kMuonBlock) / 8 + sub, rnd,
                          new_scale, c, bad);
     if (b < Q.bpm) {
       store_codes<BITS>(Q.codes, base + b, sub, c);
       if (sub == 0) Q.scales[base + b] = new_scale;
       if constexpr (OUT == 2) {
         __half* x = static_cast<__half*>(X) + (int64_t)mat * s.rows * s.ld;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = u[e] * ns.first * ns.second;
+        const uint4 h = scaled_f16(u, ns.first, ns.second);
         if ((s.cols & 7) == 0) {  // eight values of one row, and ld == cols
-          if (i < n)
-            *reinterpret_cast<uint4*>(x + i) =
-                make_uint4(pack_f16(u[0], u[1]), pack_f16(u[2], u[3]), pack_f16(u[4], u[5]),
-                           pack_f16(u[6], u[7]));
+          if (left > 0) *reinterpret_cast<uint4*>(x + i) = h;
         } else {
-          uint32_t row = (uint32_t)i / (uint32_t)s.cols;
+          const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+          const uint32_t row = (uint32_t)i / (uint32_t)s.cols;
           uint32_t col = (uint32_t)i - row * (uint32_t)s.cols;
+          uint16_t* at = reinterpret_cast<uint16_t*>(x) + (int64_t)row * s.ld + col;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            if (i + e < n) x[(int64_t)row * s.ld + col] = __float2half_rn(u[e]);
-            if (++col == (uint32_t)s.cols) { col = 0; ++row; }
+            if (e < left) *at = (uint16_t)(hw[e >> 1] >> (16 * (e & 1)));
+            ++at;
+            if (++col == (uint32_t)s.cols) {
+              col = 0;
+              at += s.ld - s.cols;
+            }
           }
         }
       } else {
@@ -121,14 +125,30 @@ direction_norm_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int n
   const bool vec = aligned16(gm);
   const int64_t base = mat * Q.bpm;
   double sum = 0.0;
-  for (int64_t b = (int64_t)part * (kThreads / 16) + half; b < Q.bpm;
-       b += (int64_t)s.parts * (kThreads / 16)) {
-    float q[8], m[8], u[8], gv[8];
-    load8<G>(gm, b * kMuonBlock + 8 * sub, n, vec, gv);
-    unpack8<BITS>(load_codes<BITS>(Q.codes, base + b, sub), q);
-    // Codes behind the last value are 0 and its gradients read as 0.
-    new_momentum(q, Q.scales[base + b], gv, beta, nesterov, m, u);
-    sum += sum_squares(u);
+  const int64_t stride = (int64_t)s.parts * (kThreads / 16);
+  for (int64_t b0 = (int64_t)part * (kThreads / 16) + half; b0 < Q.bpm; b0 += kNormUnroll * stride) {
+    uint64_t gv[kNormUnroll][4];
+    uint2 codes[kNormUnroll];
+    float scale[kNormUnroll];
+#pragma unroll
+    for (int k = 0; k < kNormUnroll; ++k) {
+      const int64_t b = b0 + k * stride;
+      codes[k] = make_uint2(0u, 0u);
+      scale[k] = 0.0f;
+      if (b < Q.bpm) {
+        codes[k] = load_codes<BITS>(Q.codes, base + b, sub);
+        scale[k] = Q.scales[base + b];
+      }
+      load8<G>(gm, b * kMuonBlock + 8 * sub, n, vec, gv[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kNormUnroll; ++k) {
+      // Codes behind the last value are 0 and its gradients read as 0.
+      uint64_t q[4], m[4], u[4];
+      unpack8<BITS>(codes[k], q);
+      new_momentum(q, scale[k], gv[k], beta, nesterov, m, u);
+      sum += sum_squares(u);
+    }
   }
   const double t = cta_sum<kThreads>(sum);
   if (threadIdx.x == 0) partials[blockIdx.x] = t;
@@ -150,12 +170,18 @@ norm_kernel(MuonShape s, MuonView x, double* partials) {
   const uint32_t per_row = (uint32_t)((cols + 7) / 8);
   const uint32_t groups = per_row * (flat ? 1u : (uint32_t)s.rows);
   double sum = 0.0;
-  for (uint64_t q = (uint64_t)part * kThreads + threadIdx.x; q < groups;
-       q += (uint64_t)s.parts * kThreads) {
-    const uint32_t row = (uint32_t)q / per_row, col = 8 * ((uint32_t)q - row * per_row);
-    float v[8];
-    load8<T>(xm + (int64_t)row * x.row_stride * es, col, cols, vec, v);
-    sum += sum_squares(v);
+  const uint64_t stride = (uint64_t)s.parts * kThreads;
+  for (uint64_t q0 = (uint64_t)part * kThreads + threadIdx.x; q0 < groups;
+       q0 += kNormUnroll * stride) {
+    uint64_t v[kNormUnroll][4];
+#pragma unroll
+    for (int k = 0; k < kNormUnroll; ++k) {
+      const uint64_t q = q0 + k * stride;
+      const uint32_t row = (uint32_t)q / per_row, col = 8 * ((uint32_t)q - row * per_row);
+      load8<T>(xm + (int64_t)row * x.row_stride * es, col, q < groups ? cols : 0, vec, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kNormUnroll; ++k) sum += sum_squares(v[k]);
   }
   const double t = cta_sum<kThreads>(sum);
   if (threadIdx.x == 0) partials[blockIdx.x] = t;
@@ -181,13 +207,10 @@ load_kernel(MuonShape s, MuonView x, const double* partials, float eps, int e0, 
   for (uint64_t q = (uint64_t)split * kThreads + threadIdx.x; q < groups;
        q += (uint64_t)splits * kThreads) {
     const uint32_t row = (uint32_t)q / per_row, col = 8 * ((uint32_t)q - row * per_row);
-    float v[8];
+    uint64_t v[4];
     load8<T>(xm + (int64_t)row * x.row_stride * es, col, s.cols, vec, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = v[e] * ns.first * ns.second;
     *reinterpret_cast<uint4*>(out + (int64_t)row * s.ld + col) =
-        make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]),
-                   pack_f16(v[6], v[7]));
+        scaled_f16(v, ns.first, ns.second);
   }
 }
 
@@ -214,10 +237,10 @@ read_kernel(MuonShape s, MuonQuant Q, void* out, int splits) {
   for (int k = 0; k < kUnroll; ++k) {
     const int64_t b = (int64_t)split * kChunkBlocks + half + k * (kThreads / 16);
     if (b < Q.bpm) {
-      float q[8];
+      uint64_t q[4];
       unpack8<BITS>(codes[k], q);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = __fmul_rn(q[e], scale[k]);
+      for (int e = 0; e < 4; ++e) q[e] = f2_mul_rn(q[e], f2_splat(scale[k]));
       store8<T>(om, b * kMuonBlock + 8 * sub, n, vec, q);
     }
   }
@@ -238,11 +261,12 @@ write_kernel(MuonShape s, MuonQuant Q, const void* values, int splits) {
 #pragma unroll
   for (int k = 0; k < kUnroll; ++k) {
     const int64_t b = (int64_t)split * kChunkBlocks + half + k * (kThreads / 16);
-    float v[8];
+    uint64_t v[4];
     load8<T>(vm, b * kMuonBlock + 8 * sub, n, vec, v);
     float top = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max_magnitude(top, v[e]);
+    for (int e = 0; e < 4; ++e)
+      top = max_magnitude(max_magnitude(top, f2_lo(v[e])), f2_hi(v[e]));
     top = half_warp_max(top);
     float scale, inverse;
     block_scale(top, Level<BITS>::recip, scale, inverse);
@@ -250,7 +274,8 @@ write_kernel(MuonShape s, MuonQuant Q, const void* values, int splits) {
     uint32_t c[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float y = fminf(fmaxf(__fmul_rn(v[e], inverse), -Level<BITS>::value),
+      const float x = (e & 1) ? f2_hi(v[e >> 1]) : f2_lo(v[e >> 1]);
+      const float y = fminf(fmaxf(__fmul_rn(x, inverse), -Level<BITS>::value),
                             Level<BITS>::value);
       c[e] = __float_as_uint(__fadd_rn(y, 12582912.0f));
     }

@@ -22,78 +22,114 @@ namespace {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Arithmetic on pairs of fp32 values (packed instructions, each half rounded
+// by itself as the scalar one is).
+__device__ __forceinline__ uint64_t f2_splat(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ uint64_t f2_add_rm(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma_rm(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // Eight consecutive values of type T from p[i ..], those at or past n as 0.
 template <int T>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, bool vec, float (&v)[8]) {
+__device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, bool vec,
+                                      uint64_t (&v)[4]) {
   if (vec && i + 8 <= n) {
     if constexpr (T == kBf16) {
       const uint4 w = ld_stream_v4(static_cast<const uint16_t*>(p) + i);
-      v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-      v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+      v[0] = f2_pack(bf16_lo(w.x), bf16_hi(w.x));
+      v[1] = f2_pack(bf16_lo(w.y), bf16_hi(w.y));
+      v[2] = f2_pack(bf16_lo(w.z), bf16_hi(w.z));
+      v[3] = f2_pack(bf16_lo(w.w), bf16_hi(w.w));
     } else {
       const float* f = static_cast<const float*>(p) + i;
       const uint4 a = ld_stream_v4(f), b = ld_stream_v4(f + 4);
-      v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
-      v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-      v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
-      v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+      v[0] = f2_pack(__uint_as_float(a.x), __uint_as_float(a.y));
+      v[1] = f2_pack(__uint_as_float(a.z), __uint_as_float(a.w));
+      v[2] = f2_pack(__uint_as_float(b.x), __uint_as_float(b.y));
+      v[3] = f2_pack(__uint_as_float(b.z), __uint_as_float(b.w));
     }
     return;
   }
+  float x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    v[e] = 0.0f;
+    x[e] = 0.0f;
     if (i + e < n) {
       if constexpr (T == kBf16)
-        v[e] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i + e] << 16);
+        x[e] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i + e] << 16);
       else
-        v[e] = static_cast<const float*>(p)[i + e];
+        x[e] = static_cast<const float*>(p)[i + e];
     }
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = f2_pack(x[2 * e], x[2 * e + 1]);
 }
 
-
 template <int T>
-__device__ __forceinline__ void store8(void* p, int64_t i, int64_t n, bool vec, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void* p, int64_t i, int64_t n, bool vec,
+                                       const uint64_t (&v)[4]) {
   if (vec && i + 8 <= n) {
     if constexpr (T == kBf16) {
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                     pack_bf16(v[6], v[7]));
+          make_uint4(pack_bf16(f2_lo(v[0]), f2_hi(v[0])), pack_bf16(f2_lo(v[1]), f2_hi(v[1])),
+                     pack_bf16(f2_lo(v[2]), f2_hi(v[2])), pack_bf16(f2_lo(v[3]), f2_hi(v[3])));
     } else {
       float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-      f[0] = make_float4(v[0], v[1], v[2], v[3]);
-      f[1] = make_float4(v[4], v[5], v[6], v[7]);
+      f[0] = make_float4(f2_lo(v[0]), f2_hi(v[0]), f2_lo(v[1]), f2_hi(v[1]));
+      f[1] = make_float4(f2_lo(v[2]), f2_hi(v[2]), f2_lo(v[3]), f2_hi(v[3]));
     }
     return;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (i + e < n) {
+      const float x = (e & 1) ? f2_hi(v[e >> 1]) : f2_lo(v[e >> 1]);
       if constexpr (T == kBf16)
-        static_cast<uint16_t*>(p)[i + e] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
+        static_cast<uint16_t*>(p)[i + e] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
       else
-        static_cast<float*>(p)[i + e] = v[e];
+        static_cast<float*>(p)[i + e] = x;
     }
 }
+// The 8 values in fp16, times two powers of two.
+__device__ __forceinline__ uint4 scaled_f16(const uint64_t (&v)[4], float first, float second) {
+  const uint64_t a = f2_splat(first), b = f2_splat(second);
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint64_t x = f2_mul_rn(f2_mul_rn(v[e], a), b);
+    w[e] = pack_f16(f2_lo(x), f2_hi(x));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
-// Levels of 8 codes as floats: the biased code in the low mantissa bits of
-// 2^23 (exact, without the quarter-rate conversion).
+// Levels of 8 codes as pairs of floats: the biased code in the low mantissa
+// bits of 2^23 (exact, without the quarter-rate conversion).
 template <int BITS>
-__device__ __forceinline__ void unpack8(uint2 w, float (&q)[8]) {
-  constexpr float bias = 8388608.0f + (BITS == 8 ? 128.0f : 8.0f);
+__device__ __forceinline__ void unpack8(uint2 w, uint64_t (&q)[4]) {
+  const uint64_t bias = f2_splat(-8388608.0f - (BITS == 8 ? 128.0f : 8.0f));
   if constexpr (BITS == 8) {
-    const uint32_t a = w.x ^ 0x80808080u, b = w.y ^ 0x80808080u;
+    const uint32_t v[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      q[e] = __uint_as_float(__byte_perm(a, 0x4B000000u, 0x7650 + e)) - bias;
-      q[4 + e] = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7650 + e)) - bias;
-    }
+    for (int e = 0; e < 4; ++e)
+      q[e] = f2_add_rn(
+          f2_pack(__uint_as_float(__byte_perm(v[e >> 1], 0x4B000000u, 0x7650 + 2 * (e & 1))),
+                  __uint_as_float(__byte_perm(v[e >> 1], 0x4B000000u, 0x7651 + 2 * (e & 1)))),
+          bias);
   } else {
-    const uint32_t a = w.x ^ 0x88888888u;
+    // Nibbles of the even and odd values, a byte each.
+    const uint32_t v = w.x ^ 0x88888888u, even = v & 0x0F0F0F0Fu, odd = (v >> 4) & 0x0F0F0F0Fu;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      q[e] = __uint_as_float(((a >> (4 * e)) & 15u) | 0x4B000000u) - bias;
+    for (int e = 0; e < 4; ++e)
+      q[e] = f2_add_rn(f2_pack(__uint_as_float(__byte_perm(even, 0x4B000000u, 0x7650 + e)),
+                               __uint_as_float(__byte_perm(odd, 0x4B000000u, 0x7650 + e))),
+                       bias);
   }
 }
 
@@ -156,46 +192,58 @@ struct Level {
 };
 
 // m' = beta m + g and U of 8 values.
-__device__ __forceinline__ void new_momentum(const float (&q)[8], float scale, const float (&g)[8],
-                                             float beta, int nesterov, float (&m)[8],
-                                             float (&u)[8]) {
+__device__ __forceinline__ void new_momentum(const uint64_t (&q)[4], float scale,
+                                             const uint64_t (&g)[4], float beta, int nesterov,
+                                             uint64_t (&m)[4], uint64_t (&u)[4]) {
+  const uint64_t s2 = f2_splat(scale), b2 = f2_splat(beta);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    m[e] = __fadd_rn(__fmul_rn(beta, __fmul_rn(q[e], scale)), g[e]);
-    u[e] = nesterov ? __fadd_rn(__fmul_rn(beta, m[e]), g[e]) : m[e];
+  for (int e = 0; e < 4; ++e) {
+    m[e] = f2_add_rn(f2_mul_rn(b2, f2_mul_rn(q[e], s2)), g[e]);
+    u[e] = m[e];
+  }
+  if (nesterov) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = f2_add_rn(f2_mul_rn(b2, m[e]), g[e]);
   }
 }
 
 // Scale and codes of a block's new momentum, of which this lane holds 8 values,
 // `left` (8 or fewer) of them inside the matrix; all lanes of a warp call it.
 template <int BITS>
-__device__ __forceinline__ void quantize_block(float (&m)[8], int left, uint64_t counter,
+__device__ __forceinline__ void quantize_block(uint64_t (&m)[4], int left, uint64_t counter,
                                                const MuonRandom& rnd, float& scale,
                                                uint32_t (&c)[8], bool& bad) {
   if (left < 8) {  // nothing is held behind the matrix's last value
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e >= left) m[e] = 0.0f;
+    for (int e = 0; e < 4; ++e)
+      m[e] = f2_pack(2 * e < left ? f2_lo(m[e]) : 0.0f, 2 * e + 1 < left ? f2_hi(m[e]) : 0.0f);
   }
   float top = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max_magnitude(top, m[e]);
+  for (int e = 0; e < 4; ++e)
+    top = max_magnitude(max_magnitude(top, f2_lo(m[e])), f2_hi(m[e]));
   top = half_warp_max(top);
   float inverse;
   block_scale(top, Level<BITS>::recip, scale, inverse);
   bad = bad || !(top < __uint_as_float(0x7F800000u));
   const uint4 w =
       philox4x32_10((uint32_t)counter, (uint32_t)(counter >> 32), rnd.t_lo, rnd.t_hi, rnd.keys);
+  const uint64_t inv2 = f2_splat(inverse), step = f2_splat(1.52587890625e-05f);
+  const uint64_t magic = f2_splat(12582784.0f);  // 1.5 2^23 - 128
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t word = chunk_word(w, e >> 1);
-    // 1 + r / 2^16, then floor(y + r / 2^16) by rounding toward -inf: first
-    // below any integer it passes, then at unit spacing near 1.5 2^23.
-    const uint32_t r = (e & 1) ? (word >> 9) & 0x007FFF80u : (word << 7) & 0x007FFF80u;
-    const float y = fminf(fmaxf(__fmul_rn(m[e], inverse), -Level<BITS>::value),
-                          Level<BITS>::value);
-    const float z = __fadd_rd(y, __uint_as_float(0x3F800000u | r));
-    c[e] = __float_as_uint(__fadd_rd(z, 12582911.0f));
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t word = chunk_word(w, e);
+    const uint64_t y = f2_mul_rn(m[e], inv2);
+    const uint64_t clamped =
+        f2_pack(fminf(fmaxf(f2_lo(y), -Level<BITS>::value), Level<BITS>::value),
+                fminf(fmaxf(f2_hi(y), -Level<BITS>::value), Level<BITS>::value));
+    // 2^23 + r for both draws; then floor(y + r / 2^16) by rounding toward -inf:
+    // y + 128 + r / 2^16 falls below no integer it passes, then unit spacing.
+    const uint64_t r = f2_pack(__uint_as_float(__byte_perm(word, 0x4B000000u, 0x7610)),
+                               __uint_as_float(__byte_perm(word, 0x4B000000u, 0x7632)));
+    const uint64_t z = f2_add_rm(f2_fma_rm(r, step, clamped), magic);
+    c[2 * e] = __float_as_uint(f2_lo(z));
+    c[2 * e + 1] = __float_as_uint(f2_hi(z));
   }
   if (left < 8) {
 #pragma unroll
@@ -208,10 +256,13 @@ __device__ __forceinline__ int left_of(int64_t i, int64_t n) {
   return (int)(i + 8 <= n ? 8 : (i < n ? n - i : 0));
 }
 
-__device__ __forceinline__ double sum_squares(const float (&v)[8]) {
+__device__ __forceinline__ double sum_squares(const uint64_t (&v)[4]) {
   double s = 0.0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s = fma((double)v[e], (double)v[e], s);
+  for (int e = 0; e < 4; ++e) {
+    s = fma((double)f2_lo(v[e]), (double)f2_lo(v[e]), s);
+    s = fma((double)f2_hi(v[e]), (double)f2_hi(v[e]), s);
+  }
   return s;
 }
 

@@ -59,11 +59,6 @@ __device__ __forceinline__ uint32_t group_address(uint32_t tile, uint32_t chunk_
   return chunk_address(tile + (uint32_t)(col >> 6) * chunk_bytes, row, (col >> 3) & 7);
 }
 
-__device__ __forceinline__ void store_half(uint32_t addr, float v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(__half_as_ushort(__float2half_rn(v)))
-               : "memory");
-}
-
 // The last product's 16 values of a lane, `left` of them inside the matrix, in
 // one row at `at` (four columns a time) or one column (32 lanes are 32
 // neighbouring columns). All loads come before the first store.
@@ -158,7 +153,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     double sum = 0.0;
     // Up to kHeld groups of 8 per thread stay in registers between the passes.
     constexpr int kHeld = 2;
-    float held[kHeld][8];
+    uint64_t held[kHeld][4];
     for (uint32_t q0 = threadIdx.x; worker && q0 < groups; q0 += kHeld * kWorkers) {
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
@@ -177,17 +172,15 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
 #pragma unroll 1
     for (uint32_t q = threadIdx.x, k = 0; worker && q < groups; q += kWorkers, ++k) {
       const uint32_t row = q / per_row, col = 8 * (q - row * per_row);
-      float v[8];
+      uint64_t v[4];
       if (groups > kHeld * kWorkers) {
         load8<T>(xm + (int64_t)row * x.row_stride * es, col, sh.cols, vec, v);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = k == 0 ? held[0][e] : held[1][e];
+        for (int e = 0; e < 4; ++e) v[e] = k == 0 ? held[0][e] : held[1][e];
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * ns.first * ns.second;
-      st_shared(group_address(X, p.xs, (int)row, (int)col), pack_f16(v[0], v[1]),
-                pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+      const uint4 h = scaled_f16(v, ns.first, ns.second);
+      st_shared(group_address(X, p.xs, (int)row, (int)col), h.x, h.y, h.z, h.w);
     }
   } else {
     const int half = threadIdx.x >> 4, sub = threadIdx.x & 15;
@@ -198,7 +191,8 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     // registers between the passes.
     constexpr int kHeld = 3;
     constexpr int kChunk = kHeld * (kWorkers / 16);
-    float gv[kHeld][8], scale[kHeld];
+    uint64_t gv[kHeld][4];
+    float scale[kHeld];
     uint2 codes[kHeld];
     auto fetch = [&](int64_t b0) {
 #pragma unroll
@@ -218,7 +212,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
       fetch(b0);
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
-        float q[8], m[8], u[8];
+        uint64_t q[4], m[4], u[4];
         unpack8<BITS>(codes[k], q);
         new_momentum(q, scale[k], gv[k], beta, nesterov, m, u);
         sum += sum_squares(u);
@@ -237,7 +231,8 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
         if (b0 + 2 * warp + k * (kWorkers / 16) >= Q.bpm) break;
         const int64_t i = b * kMuonBlock + 8 * sub;
         const int left = left_of(i, n);
-        float q[8], m[8], u[8], now[8], old_scale = 0.0f, new_scale;
+        uint64_t q[4], m[4], u[4], now[4];
+        float old_scale = 0.0f, new_scale;
         uint2 old_codes = make_uint2(0u, 0u);
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
@@ -245,7 +240,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
             old_codes = codes[h];
             old_scale = scale[h];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) now[e] = gv[h][e];
+            for (int e = 0; e < 4; ++e) now[e] = gv[h][e];
           }
         unpack8<BITS>(old_codes, q);
         new_momentum(q, old_scale, now, beta, nesterov, m, u);
@@ -257,16 +252,18 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
           if (sub == 0) Q.scales[base + b] = new_scale;
           int row = (int)((uint32_t)i / (uint32_t)sh.cols);
           int col = (int)i - row * sh.cols;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] = u[e] * ns.first * ns.second;
+          const uint4 h = scaled_f16(u, ns.first, ns.second);
           if ((sh.cols & 7) == 0) {  // eight values of one row
-            if (left > 0)
-              st_shared(group_address(X, p.xs, row, col), pack_f16(u[0], u[1]),
-                        pack_f16(u[2], u[3]), pack_f16(u[4], u[5]), pack_f16(u[6], u[7]));
+            if (left > 0) st_shared(group_address(X, p.xs, row, col), h.x, h.y, h.z, h.w);
           } else {
+            const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              if (e < left) store_half(group_address(X, p.xs, row, col) + 2u * (col & 7), u[e]);
+              if (e < left)
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(group_address(X, p.xs, row, col) +
+                                                             2u * (col & 7)),
+                             "h"((uint16_t)(hw[e >> 1] >> (16 * (e & 1))))
+                             : "memory");
               if (++col == sh.cols) {
                 col = 0;
                 ++row;
