@@ -83,15 +83,17 @@ cudaError_t muon_launch_write(const MuonShape& s, const MuonQuant& q, const void
                               cudaStream_t st);
 
 // ---------------------------------------------------------------- products
-// The iteration of one group of matrices, X_0 being in the stack's x[0].
-struct MuonStack {
-  void* x[2];                  // fp16 [batch][rows][ld], the steps alternate
-  void *a, *p;                 // fp16 [batch][s][lds], s the short side
-  int32_t ld, lds;
-};
-
 struct MuonNs {
   int32_t rows, cols, batch, steps;
+  // fp16 matrices: X [batch][rows][ld] of even and odd steps (X_0 in x[0]); A and
+  // P [batch][s][lds], s the short side.
+  void* x[2];
+  void *a, *p;
+  int32_t ld, lds;
+  // Items that share a tile of A's contraction and that add the shares up (a
+  // power of two up to 16); fp32 [batch][tile][split][256 or 128 squared].
+  int32_t split, reduce;
+  float* partials;
   // Power-of-two scales and coefficients of each step's products.
   float gram_alpha[kMuonMaxSteps];
   float poly_alpha[kMuonMaxSteps], poly_mid[kMuonMaxSteps], poly_diag[kMuonMaxSteps];
@@ -107,7 +109,8 @@ struct MuonNs {
   uint64_t wait_ns;            // longest wait inside the kernel before it gives up
 };
 
-cudaError_t muon_launch_ns(const MuonStack& m, const MuonNs& g, cudaStream_t st);
+// On output tiles of bn = 256 (CTA pairs) or 128.
+cudaError_t muon_launch_ns(const MuonNs& g, int bn, cudaStream_t st);
 
 // Matrices that fit a CTA's shared memory: the whole operator in one launch, a
 // CTA each. Shared memory it takes, 0 where a matrix does not fit.

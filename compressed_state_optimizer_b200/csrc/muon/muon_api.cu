@@ -19,6 +19,11 @@ static_assert(MUA_STATUS_NONFINITE == mua::kMuonNonFinite &&
                   MUA_STATUS_TIMEOUT == mua::kMuonTimeout,
               "status bits");
 
+struct Tiling {               // of the products: see tiling()
+  int32_t bn, split, reduce;
+  double us;
+};
+
 struct mua_muon_ctx {
   int32_t rows, cols, count, bits, steps;
   int32_t s;                 // short side: A and P are s x s
@@ -26,9 +31,10 @@ struct mua_muon_ctx {
   bool small;                // one CTA holds a matrix on chip
   int32_t ld, lds;           // fp16 row strides of X and of A, P
   int32_t group, parts;
+  Tiling tiling;
   int64_t bpm;               // blocks of one matrix
   int64_t off_scales, off_codes, state_bytes;
-  int64_t off_partials, off_factor, off_counters, off_x[2], off_a, off_p, workspace_bytes;
+  int64_t off_partials, off_factor, off_counters, off_x[2], off_a, off_p, off_split, workspace_bytes;
   float coef[mua::kMuonMaxSteps][3];
   int32_t ex[mua::kMuonMaxSteps + 1], ea[mua::kMuonMaxSteps], ep[mua::kMuonMaxSteps];
   int64_t wait_ns;
@@ -39,7 +45,7 @@ namespace {
 thread_local char g_error[256] = "no CUDA error";
 
 constexpr int64_t kDefaultWaitNs = 2000000000;
-constexpr int64_t kGroupBytes = 32 << 20;  // X of one group
+constexpr int64_t kGroupBytes = 64 << 20;  // X of one group
 
 int fail(cudaError_t e, const char* where) {
   std::snprintf(g_error, sizeof g_error, "%s: %s", where, cudaGetErrorString(e));
@@ -170,16 +176,48 @@ mua::MuonNs iteration(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t
 // Its launch, X_0 and its factors being in the workspace.
 int iterate(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count, const Target& to,
             uint32_t* status, cudaStream_t st) {
-  mua::MuonStack m;
-  m.x[0] = ws + h->off_x[0];
-  m.x[1] = ws + h->off_x[1];
-  m.a = ws + h->off_a;
-  m.p = ws + h->off_p;
-  m.ld = h->ld;
-  m.lds = h->lds;
-  const cudaError_t e =
-      mua::muon_launch_ns(m, iteration(h, ws, first, count, to, status), st);
+  mua::MuonNs g = iteration(h, ws, first, count, to, status);
+  g.x[0] = ws + h->off_x[0];
+  g.x[1] = ws + h->off_x[1];
+  g.a = ws + h->off_a;
+  g.p = ws + h->off_p;
+  g.ld = h->ld;
+  g.lds = h->lds;
+  g.split = h->tiling.split;
+  g.reduce = h->tiling.reduce;
+  g.partials = reinterpret_cast<float*>(ws + h->off_split);
+  const cudaError_t e = mua::muon_launch_ns(g, h->tiling.bn, st);
   return e == cudaSuccess ? MUA_OK : fail(e, "Newton-Schulz kernel launch");
+}
+
+// Time of a step's products on tiles of bn, in us: per product the waves of
+// items over the SMs, an item's k-slices or (where longer) its epilogue, and the
+// way from one product's last store to the next one's first MMA. Measured: a
+// 64-deep slice 0.33 us on 256 x 256 tiles of CTA pairs, 0.21 us on 128 x 128;
+// an epilogue 1.5 and 0.9 us; between products 3.5 us. The larger tile wins
+// from about 2048 x 2048 or 8 x 1024 x 1024 on, the smaller one below
+// (512 x 512: 103 against 126 us, 16 x 300 x 300: 100 against 147 us).
+Tiling tiling(int32_t rows, int32_t cols, int32_t batch, int32_t bn) {
+  const bool big = bn == 256;
+  const double slice = big ? 0.33 : 0.21, epilogue = big ? 1.5 : 0.9, between = 3.5;
+  const int64_t units = big ? 74 : 148;  // CTA pairs or CTAs of a B200
+  const int64_t s = std::min(rows, cols), l = std::max(rows, cols);
+  const int64_t tm = (s + bn - 1) / bn, sym = tm * (tm + 1) / 2 * batch;
+  const int64_t upd = (int64_t)((rows + bn - 1) / bn) * ((cols + bn - 1) / bn) * batch;
+  const int64_t gram = (l + 63) / 64, update = (s + 63) / 64;
+  Tiling t = {bn, 1, 1, 0.0};
+  // A's tiles split over idle SMs while a share keeps 8 slices.
+  const int64_t split = std::min<int64_t>(std::min<int64_t>(16, units / sym), gram / 8);
+  if (split > 1) {
+    t.split = (int32_t)split;
+    while (2 * t.reduce <= t.split) t.reduce *= 2;
+  }
+  auto product = [&](int64_t items, int64_t slices) {
+    return (double)((items + units - 1) / units) * std::max(slices * slice, epilogue) + between;
+  };
+  t.us = product(sym * t.split, gram / t.split) + product(sym, update) + product(upd, update);
+  if (t.split > 1) t.us += epilogue + between;
+  return t;
 }
 
 int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t steps,
@@ -228,9 +266,14 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
   h->off_codes = h->off_scales + round_up(4 * count * bpm, 256);
   h->state_bytes = h->off_codes + count * bpm * mua::kMuonBlock * bits / 8;
   const int64_t x_bytes = (int64_t)rows * h->ld * 2, a_bytes = (int64_t)s * h->lds * 2;
-  const int64_t fit = std::max<int64_t>(1, std::min<int64_t>(count, kGroupBytes / x_bytes));
-  const int64_t groups = (count + fit - 1) / fit;
+  const int64_t items = 16 * (((int64_t)s + 127) / 128 * (((int64_t)s + 127) / 128 + 1) * 17 +
+                              (((int64_t)rows + 127) / 128) * (((int64_t)cols + 127) / 128));
+  const int64_t fit = std::max<int64_t>(
+      1, std::min<int64_t>(std::min<int64_t>(count, kGroupBytes / x_bytes), (1 << 30) / items));
+  const int64_t groups = (count + fit - 1) / fit;  // items of a launch fit 31 bits
   h->group = (int32_t)((count + groups - 1) / groups);
+  const Tiling narrow = tiling(rows, cols, h->group, 128), wide = tiling(rows, cols, h->group, 256);
+  h->tiling = wide.us <= narrow.us ? wide : narrow;
   h->parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(mua::kMuonMaxParts, n / 16384));
   int64_t at = 256;
   auto take = [&at](int64_t bytes) {
@@ -245,6 +288,11 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
   h->off_x[1] = steps > 1 ? take(h->group * x_bytes) : h->off_x[0];
   h->off_a = take(h->group * a_bytes);
   h->off_p = take(h->group * a_bytes);
+  const int64_t tm = (s + h->tiling.bn - 1) / h->tiling.bn;
+  h->off_split = h->tiling.split > 1
+                     ? take(4ll * h->group * (tm * (tm + 1) / 2) * h->tiling.split *
+                            h->tiling.bn * h->tiling.bn)
+                     : at;
   h->workspace_bytes = at;
   h->wait_ns = kDefaultWaitNs;
   *out = h;

@@ -16,10 +16,13 @@
 // A tile is 256 x 256 on a pair of CTAs (cta_group::2: each SM holds half of
 // both operands, 8 KB of shared memory read per 16-deep MMA and SM instead of
 // 12) or 128 x 128 on one CTA when the 256-wide tiles would be too few for the
-// SMs. Per CTA: warp 0 streams 64-deep operand slices into a ring of 128-byte
-// swizzled shared tiles (TMA), warp 1 issues the MMAs, warps 2..9 turn
-// finished accumulators into output while the next tile's MMAs run into the
-// other half of TMEM.
+// SMs. Per CTA: warps 0 and 10 stream 64-deep slices of the operands A and B
+// into a ring of 128-byte swizzled shared tiles (TMA), warp 1 issues the MMAs,
+// warps 2..9 turn finished accumulators into output while the next tile's MMAs
+// run into the other half of TMEM. The instructions between two slices' MMAs are
+// what bounds the rate next to the tensor cores (256 cycles of MMA a slice on
+// 128 x 128, 512 on 256 x 256): hence a warp for each operand, one copy for an
+// operand whose rows are contiguous in depth, and majors fixed per item.
 //
 // Every wait is bounded by the global timer. A wait that runs out sets
 // MUA_STATUS_TIMEOUT, the CTA's roles stop, copies and MMAs in flight are
@@ -32,8 +35,9 @@ namespace mua {
 namespace {
 
 constexpr int kEpilogueWarps = 8;            // two for each quarter of the TMEM lanes
-constexpr int kThreads = 64 + 32 * kEpilogueWarps;
-constexpr int kStageBytes = 32768;           // 128 rows of A and of B, 64 deep
+constexpr int kThreads = 96 + 32 * kEpilogueWarps;
+constexpr int kOperandBytes = 16384;         // 128 rows of an operand, 64 deep
+constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kChunkBytes = 4096;            // 32 rows x 64 fp16 columns of output
 template <int BN>
 struct Ring {
@@ -43,11 +47,10 @@ struct Ring {
       stages * kStageBytes + kEpilogueWarps * chunks * kChunkBytes + 1024;  // + alignment
 };
 struct Maps {
-  CUtensorMap load_x[2], load_a, load_p;     // boxes of 64 x 64
-  CUtensorMap store_x[2], store_a, store_p;  // 64 x 32
+  // X of even and odd steps, A, P: boxes of 64 columns by 128 rows (an operand's
+  // rows), 64 rows (its columns) and 32 rows (the epilogue's copies).
+  CUtensorMap rows[4], cols[4], store[4];
 };
-
-enum Product : int { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 // Tiles of one matrix in a symmetric product (the lower block triangle) and in
 // an update.
@@ -71,29 +74,73 @@ __device__ __forceinline__ Tiles tiles_of(const MuonNs& g) {
 }
 
 // Work item w of the launch, in the order (step, product, matrix, tile): tile
-// (i, j) of a product of matrix z, which needs `before` finished tiles of z.
-// The triangle is walked row by row; the update walks the short side's tiles
-// first, so that tiles in flight share their slice of X.
+// (i, j) of a product of matrix z over k-slices kb0 .. kb1 - 1, which needs
+// `before` finished items of z. The triangle is walked row by row; the update
+// walks the short side's tiles first, so that tiles in flight share their slice
+// of X. Where A's tiles are too few for the SMs, `split` items share one's
+// contraction and leave fp32 partial sums, and `reduce` items add them up, in
+// a fixed order, a share of the tile's rows each.
+enum Product : int { kGram = 0, kReduce = 1, kPoly = 2, kUpdate = 3 };
 struct Item {
-  int step, kind, z, i, j, kblocks;
+  int step, kind, z, tile, share, i, j, kb0, kb1;
   uint32_t before;
   bool last;
 };
-__device__ __forceinline__ int64_t item_count(const MuonNs& g, const Tiles& T) {
-  return (int64_t)(2 * T.sym + T.upd) * g.batch * g.steps;
+struct Counts {  // items of one matrix in a step
+  uint32_t gram, reduce, poly, update, step;
+};
+__device__ __forceinline__ Counts counts_of(const MuonNs& g, const Tiles& T) {
+  Counts c;
+  c.gram = (uint32_t)(T.sym * g.split);
+  c.reduce = g.split > 1 ? (uint32_t)(T.sym * g.reduce) : 0u;
+  c.poly = (uint32_t)T.sym;
+  c.update = (uint32_t)T.upd;
+  c.step = c.gram + c.reduce + c.poly + c.update;
+  return c;
 }
-__device__ __forceinline__ Item item_of(const MuonNs& g, const Tiles& T, int64_t w) {
+__device__ __forceinline__ Item item_of(const MuonNs& g, const Tiles& T, const Counts& C,
+                                        uint32_t w) {
   Item it;
-  const int64_t sym = (int64_t)T.sym * g.batch, per = 2 * sym + (int64_t)T.upd * g.batch;
-  it.step = (int)(w / per);
-  int64_t r = w - it.step * per;
-  it.kind = r < sym ? kGram : (r < 2 * sym ? kPoly : kUpdate);
-  r -= it.kind * sym;
-  const int tiles = it.kind == kUpdate ? T.upd : T.sym;
-  it.z = (int)(r / tiles);
-  const int t = (int)(r - (int64_t)it.z * tiles);
-  it.before = (uint32_t)(it.step * (2 * T.sym + T.upd) + it.kind * T.sym);
-  it.kblocks = it.kind == kGram ? T.gram : T.update;
+  const uint32_t batch = (uint32_t)g.batch;
+  it.step = (int)(w / (C.step * batch));
+  uint32_t r = w - (uint32_t)it.step * C.step * batch, per = C.gram;
+  it.before = (uint32_t)it.step * C.step;
+  it.kind = kGram;
+  if (r >= per * batch) {
+    r -= per * batch;
+    it.before += per;
+    per = C.reduce;
+    it.kind = kReduce;
+    if (r >= per * batch) {
+      r -= per * batch;
+      it.before += per;
+      per = C.poly;
+      it.kind = kPoly;
+      if (r >= per * batch) {
+        r -= per * batch;
+        it.before += per;
+        per = C.update;
+        it.kind = kUpdate;
+      }
+    }
+  }
+  it.z = (int)(r / per);
+  int t = (int)(r - (uint32_t)it.z * per);
+  it.share = 0;
+  it.kb0 = 0;
+  it.kb1 = T.update;
+  if (it.kind == kGram) {
+    const int tile = t / g.split;
+    it.share = t - tile * g.split;
+    t = tile;
+    it.kb0 = it.share * T.gram / g.split;
+    it.kb1 = (it.share + 1) * T.gram / g.split;
+  } else if (it.kind == kReduce) {
+    const int tile = t / g.reduce;
+    it.share = t - tile * g.reduce;
+    t = tile;
+  }
+  it.tile = t;
   it.last = it.kind == kUpdate && it.step == g.steps - 1;
   if (it.kind == kUpdate) {
     if (g.rows <= g.cols) {
@@ -111,16 +158,16 @@ __device__ __forceinline__ Item item_of(const MuonNs& g, const Tiles& T, int64_t
   }
   return it;
 }
-// Whether slice kb of the operand with M / N block `block` is read with its
-// M / N index contiguous. X has one major per product; A and P (symmetric)
-// are read from below the diagonal.
+// First k-slice of an item whose operand (A or B) is read with its M / N index
+// contiguous. X has one major per product; A and P (symmetric) are read from
+// below the diagonal, as rows up to the diagonal block and columns behind it.
 template <int BN>
-__device__ __forceinline__ bool reads_mn(const MuonNs& g, int kind, bool a, int block, int kb) {
+__device__ __forceinline__ int first_mn(const MuonNs& g, const Item& it, bool a) {
+  constexpr int never = 1 << 30;
   const bool tall = g.rows > g.cols;
-  if (kind == kGram) return tall;
-  const bool symmetric = kind == kPoly || a != tall;
-  if (symmetric) return kb * 64 / BN > block;
-  return !tall;  // X: the B operand of a wide update
+  if (it.kind == kGram) return tall ? 0 : never;
+  if (it.kind == kPoly || a != tall) return ((a ? it.i : it.j) + 1) * (BN / 64);
+  return tall ? never : 0;
 }
 
 // Waits until matrix z has `tiles` finished tiles (every epilogue warp of a
@@ -145,6 +192,40 @@ __device__ __forceinline__ bool matrix_wait(const MuonNs& g, int z, uint32_t wan
   }
 }
 
+// This warp's part of an item is in memory: count it.
+__device__ __forceinline__ void count_item(const MuonNs& g, int z) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.counters + z) : "memory");
+}
+
+// This warp's rows of a share of a split tile of A: the partial sums in the
+// order of the splits, scaled and rounded to fp16. A lane takes 8 columns.
+template <int CG, int BN>
+__device__ __forceinline__ void reduce_rows(const MuonNs& g, const Tiles& T, const Item& it,
+                                            uint32_t rank, int warp, int lane, float alpha) {
+  const int s = min(g.rows, g.cols);
+  const int share = 128 / g.reduce;  // rows of the tile's 128 of this CTA
+  const float* from = g.partials + ((int64_t)it.z * T.sym + it.tile) * g.split * (BN * BN);
+  const int group = BN == 256 ? lane : lane & 15;
+  const int col = it.j * BN + 8 * group;
+  for (int q = warp * (256 / BN) + (BN == 256 ? 0 : lane >> 4); q < share;
+       q += kEpilogueWarps * (256 / BN)) {
+    const int r = (int)rank * 128 + it.share * share + q, row = it.i * BN + r;
+    if (row >= s || col >= s) continue;
+    float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f), hi = lo;
+#pragma unroll 4
+    for (int k = 0; k < g.split; ++k) {
+      const float4* p =
+          reinterpret_cast<const float4*>(from + (int64_t)k * (BN * BN) + r * BN + 8 * group);
+      const float4 a = __ldcg(p), b = __ldcg(p + 1);
+      lo.x += a.x; lo.y += a.y; lo.z += a.z; lo.w += a.w;
+      hi.x += b.x; hi.y += b.y; hi.z += b.z; hi.w += b.w;
+    }
+    *reinterpret_cast<uint4*>(static_cast<__half*>(g.a) + ((int64_t)it.z * s + row) * g.lds + col) =
+        make_uint4(pack_f16(lo.x * alpha, lo.y * alpha), pack_f16(lo.z * alpha, lo.w * alpha),
+                   pack_f16(hi.x * alpha, hi.y * alpha), pack_f16(hi.z * alpha, hi.w * alpha));
+  }
+}
+
 template <int CG, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
 ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
@@ -154,17 +235,19 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drained;
   __shared__ __align__(8) uint64_t addend_full[kEpilogueWarps][kChunks];
-  __shared__ uint32_t tmem_base_s, stop, issued_s, peer_issued_s;
+  __shared__ uint32_t tmem_base_s, stop;
+  __shared__ uint32_t issued_s[4];  // copies of A and of B, of this CTA and the pair's other
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? (blockIdx.x & 1u) : 0u;
-  const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const uint32_t first = blockIdx.x / CG, stride = gridDim.x / CG;
   const Tiles tiles = tiles_of<BN>(g);
-  const int64_t items = item_count(g, tiles);
+  const Counts counts = counts_of(g, tiles);
+  const uint32_t items = counts.step * (uint32_t)(g.batch * g.steps);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full[s]), CG);
+      mbar_init(smem_u32(&full[s]), 2 * CG);
       mbar_init(smem_u32(&empty[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -175,7 +258,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
       for (int c = 0; c < kChunks; ++c) mbar_init(smem_u32(&addend_full[w][c]), 1);
     mbar_init(smem_u32(&drained), 1);
     stop = 0;
-    issued_s = peer_issued_s = 0;
+    for (int k = 0; k < 4; ++k) issued_s[k] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -200,14 +283,26 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
   const uint32_t tmem = tmem_base_s;
   volatile uint32_t* stop_v = &stop;
 
-  // Warps 0 and 1 run their loops converged; an elected lane issues.
-  if (warp == 0) {
+  // The producing and issuing warps run their loops converged; an elected lane
+  // issues.
+  if (warp == 0 || warp == kThreads / 32 - 1) {
+    const bool is_a = warp == 0;
+    const uint32_t lead = CG == 2 && rank != 0 ? peer_address(smem_u32(&full[0]), 0) : 0;
     uint32_t issued = 0, s = 0, turn = 1;
     bool ok = true;
     int ready_z = -1;
     uint32_t ready = 0;
-    for (int64_t w = first; ok && w < items; w += stride) {
-      const Item it = item_of(g, tiles, w);
+    for (uint32_t w = first; ok && w < items; w += stride) {
+      const Item it = item_of(g, tiles, counts, w);
+      if (it.kind == kReduce) continue;
+      const bool tall = g.rows > g.cols;
+      const int mn_from = first_mn<BN>(g, it, is_a);
+      const int which = it.kind == kGram || (it.kind == kUpdate && is_a == tall)
+                            ? (it.step & 1)
+                            : (it.kind == kPoly ? 2 : 3);
+      const CUtensorMap *rows_map = &maps.rows[which], *cols_map = &maps.cols[which];
+      const int m0 = is_a ? it.i * BN + (int)rank * 128          // this CTA's rows of A
+                          : it.j * BN + (int)rank * (BN / CG);   // and of B
       if (it.z != ready_z || it.before != ready) {
         ok = matrix_wait(g, it.z, it.before * (CG * kEpilogueWarps), stop_v);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -216,37 +311,24 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
         ready_z = it.z;
         ready = it.before;
       }
-      const bool tall = g.rows > g.cols;
-      const CUtensorMap* x = &maps.load_x[it.step & 1];
-      const CUtensorMap* ma = it.kind == kGram ? x : (it.kind == kPoly ? &maps.load_a
-                                                                       : (tall ? x : &maps.load_p));
-      const CUtensorMap* mb = it.kind == kGram ? x : (it.kind == kPoly ? &maps.load_a
-                                                                       : (tall ? &maps.load_p : x));
-      const int a0 = it.i * BN + (int)rank * 128;         // this CTA's rows of A
-      const int b0 = it.j * BN + (int)rank * (BN / CG);   // and of B
-      for (int kb = 0; kb < it.kblocks; ++kb) {
-        ok = mbar_wait(smem_u32(&empty[s]), turn, g.wait_ns, stop_v);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+      for (int kb = it.kb0; kb < it.kb1; ++kb) {
+        ok = mbar_wait_warp(smem_u32(&empty[s]), turn, g.wait_ns, stop_v);
         if (!ok) break;
-        const uint32_t a = ring + s * kStageBytes, b = a + 16384;
-        const bool a_mn = reads_mn<BN>(g, it.kind, true, it.i, kb);
-        const bool b_mn = reads_mn<BN>(g, it.kind, false, it.j, kb);
+        const uint32_t to = ring + s * kStageBytes + (is_a ? 0 : kOperandBytes);
         if (elect_one()) {
           uint32_t bar = smem_u32(&full[s]);
           if (CG == 2 && rank != 0) {
-            bar = peer_address(bar, 0);
-            mbar_expect_cluster(bar, kStageBytes);
+            bar = lead + 8 * s;
+            mbar_expect_cluster(bar, kOperandBytes);
           } else {
-            mbar_expect(bar, kStageBytes);
+            mbar_expect(bar, kOperandBytes);
           }
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            tma_load<CG>(a + q * 8192, ma, bar, a_mn ? a0 + 64 * q : kb * 64,
-                         a_mn ? kb * 64 : a0 + 64 * q, it.z);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            tma_load<CG>(b + q * 8192, mb, bar, b_mn ? b0 + 64 * q : kb * 64,
-                         b_mn ? kb * 64 : b0 + 64 * q, it.z);
+          if (kb >= mn_from) {
+            tma_load<CG>(to, cols_map, bar, m0, kb * 64, it.z);
+            tma_load<CG>(to + 8192, cols_map, bar, m0 + 64, kb * 64, it.z);
+          } else {
+            tma_load<CG>(to, rows_map, bar, kb * 64, m0, it.z);
+          }
         }
         __syncwarp();
         ++issued;
@@ -257,10 +339,10 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
       }
     }
     if (elect_one()) {
-      issued_s = issued;
+      issued_s[is_a ? 0 : 1] = issued;
       if (CG == 2 && rank != 0)
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                         peer_address(smem_u32(&peer_issued_s), 0)),
+                         peer_address(smem_u32(&issued_s[is_a ? 2 : 3]), 0)),
                      "r"(issued)
                      : "memory");
     }
@@ -268,29 +350,29 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
     if (rank == 0) {
       uint32_t n = 0, s = 0, turn = 0;
       bool ok = true;
-      for (int64_t w = first; ok && w < items; w += stride, ++n) {
-        const Item it = item_of(g, tiles, w);
+      for (uint32_t w = first; ok && w < items; w += stride) {
+        const Item it = item_of(g, tiles, counts, w);
+        if (it.kind == kReduce) continue;
         const uint32_t acc = n & 1u;
         ok = mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1u) ^ 1u, g.wait_ns, stop_v);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         fence_after();
         const uint32_t d = tmem + acc * BN;
-        for (int kb = 0; kb < it.kblocks; ++kb) {
-          ok = mbar_wait(smem_u32(&full[s]), turn, g.wait_ns, stop_v);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          fence_after();
-          const uint32_t a = ring + s * kStageBytes, b = a + 16384;
-          const bool a_mn = reads_mn<BN>(g, it.kind, true, it.i, kb);
-          const bool b_mn = reads_mn<BN>(g, it.kind, false, it.j, kb);
+        const int a_from = first_mn<BN>(g, it, true), b_from = first_mn<BN>(g, it, false);
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+          const uint32_t a = ring + s * kStageBytes, b = a + kOperandBytes;
+          const bool a_mn = kb >= a_from, b_mn = kb >= b_from;
           const uint32_t idesc = instruction_desc<CG>(BN, a_mn, b_mn);
           const uint64_t da = operand_desc(a, 8192), db = operand_desc(b, 8192);
           const uint64_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+          ok = mbar_wait_warp(smem_u32(&full[s]), turn, g.wait_ns, stop_v);
+          if (!ok) break;
+          fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f16<CG>(d, da + k * sa, db + k * sb, idesc, (kb | k) != 0);
+              mma_f16<CG>(d, da + k * sa, db + k * sb, idesc, kb != it.kb0 || k != 0);
             mma_commit<CG>(smem_u32(&empty[s]));
           }
           __syncwarp();
@@ -301,6 +383,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
         }
         if (ok && elect_one()) mma_commit<CG>(smem_u32(&acc_full[acc]));
         __syncwarp();
+        ++n;
       }
       // The MMAs in flight end before TMEM and the operands go.
       if (elect_one()) {
@@ -323,16 +406,14 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
     int ready_z = -1;
     uint32_t ready = 0;
     bool ok = true;
-    for (int64_t w = first; ok && w < items; w += stride, ++n) {
-      const Item it = item_of(g, tiles, w);
+    for (uint32_t w = first; ok && w < items; w += stride) {
+      const Item it = item_of(g, tiles, counts, w);
       const int M = it.kind == kUpdate ? g.rows : min(g.rows, g.cols);
       const int N = it.kind == kUpdate ? g.cols : M;
       const int row0 = it.i * BN + (int)rank * 128 + quarter * 32;
       const int col0 = it.j * BN + side * (BN / 2);
       const int chunks = row0 < M ? max(0, min(kChunks, (N - col0 + 63) / 64)) : 0;
-      const uint32_t acc = n & 1u;
-      if (it.kind == kPoly && chunks > 0) {
-        // The addend on its way while the MMAs run.
+      if ((it.kind == kPoly && chunks > 0) || it.kind == kReduce) {
         if (it.z != ready_z || it.before != ready) {
           ok = matrix_wait(g, it.z, it.before * (CG * kEpilogueWarps), stop_v);
           ok = __all_sync(0xFFFFFFFFu, ok);
@@ -341,11 +422,28 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
           ready_z = it.z;
           ready = it.before;
         }
+      }
+      float f = it.step == 0 && it.kind != kPoly ? g.factor[it.z] : 1.0f;
+      if (it.kind <= kReduce) f *= f;
+      const float alpha = f * (it.kind <= kReduce ? g.gram_alpha[it.step]
+                                                  : (it.kind == kPoly ? g.poly_alpha[it.step]
+                                                                      : g.update_alpha[it.step]));
+      if (it.kind == kReduce) {
+        reduce_rows<CG, BN>(g, tiles, it, rank, warp - 2, lane, alpha);
+        __syncwarp();
+        if (lane == 0) count_item(g, it.z);
+        continue;
+      }
+      const uint32_t acc = n & 1u;
+      if (it.kind == kPoly && chunks > 0) {
+        // The addend on its way while the MMAs run.
+        fence_async_shared();
+        __syncwarp();
         if (lane == 0) {
           for (int c = 0; c < chunks; ++c) {
             const uint32_t bar = smem_u32(&addend_full[warp - 2][c]);
             mbar_expect(bar, kChunkBytes);
-            tma_load<1>(stage + c * kChunkBytes, &maps.store_a, bar, col0 + 64 * c, row0, it.z);
+            tma_load<1>(stage + c * kChunkBytes, &maps.store[2], bar, col0 + 64 * c, row0, it.z);
           }
         }
         asked = (1u << chunks) - 1u;
@@ -356,17 +454,11 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
       fence_after();
       const uint32_t lanes =
           tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + side * (BN / 2);
-      float f = it.step == 0 && it.kind != kPoly ? g.factor[it.z] : 1.0f;
-      if (it.kind == kGram) f *= f;
-      const float alpha = f * (it.kind == kGram ? g.gram_alpha[it.step]
-                                                : (it.kind == kPoly ? g.poly_alpha[it.step]
-                                                                    : g.update_alpha[it.step]));
-      if (!it.last) {
+      const bool partial = it.kind == kGram && g.split > 1;
+      if (!it.last && !partial) {
         const float mid = g.poly_mid[it.step], diag = g.poly_diag[it.step];
-        const CUtensorMap* out = it.kind == kGram
-                                     ? &maps.store_a
-                                     : (it.kind == kPoly ? &maps.store_p
-                                                         : &maps.store_x[(it.step & 1) ^ 1]);
+        const CUtensorMap* out =
+            &maps.store[it.kind == kGram ? 2 : (it.kind == kPoly ? 3 : (it.step & 1) ^ 1)];
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
           const uint32_t tile = stage + c * kChunkBytes;
@@ -410,6 +502,28 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
           __syncwarp();
           if (lane == 0) tma_store(out, tile, col0 + 64 * c, row0, it.z);
         }
+      } else if (partial) {
+        float* out = g.partials +
+                     (((int64_t)it.z * tiles.sym + it.tile) * g.split + it.share) * (BN * BN) +
+                     (int)(rank * 128 + quarter * 32) * BN + side * (BN / 2);
+#pragma unroll 1
+        for (int c = 0; c < 2 * chunks; ++c) {
+          uint32_t v[32];
+          tmem_load32(lanes + 32 * c, v);
+          tmem_load_wait();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_shared(chunk_address(stage, lane, q), v[4 * q], v[4 * q + 1], v[4 * q + 2],
+                      v[4 * q + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int r = 4 * q + (lane >> 3);
+            *reinterpret_cast<uint4*>(out + r * BN + 32 * c + 4 * (lane & 7)) =
+                ld_shared(chunk_address(stage, r, lane & 7));
+          }
+          __syncwarp();
+        }
       } else {
         // 32 x 32 fp32 through shared memory: a lane then holds four columns,
         // eight lanes a row's 128 (64) contiguous bytes.
@@ -452,13 +566,12 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
         else
           mbar_arrive(smem_u32(&acc_empty[acc]));
         if (!it.last) {
-          // This warp's part of the tile is in memory: count it.
           tma_store_wait_all();
-          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.counters + it.z)
-                       : "memory");
+          count_item(g, it.z);
         }
       }
       __syncwarp();
+      ++n;
     }
     for (int c = 0; c < kChunks; ++c)
       if (asked >> c & 1u)
@@ -468,13 +581,18 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
   fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
-  // Operand copies land before their shared memory goes. A pair's copies count
-  // on the first CTA's barriers, one arrival from each CTA: where the two gave
-  // up at different slices the missing arrivals are made here.
+  // Operand copies land before their shared memory goes. A slice's barrier counts
+  // an arrival per operand and CTA: where the producers gave up at different
+  // slices the missing arrivals are made here.
   if (threadIdx.x == 0 && rank == 0) {
-    const uint32_t mine = issued_s, other = CG == 2 ? peer_issued_s : mine;
-    const uint32_t most = max(mine, other);
-    for (uint32_t c = min(mine, other); c < most; ++c) mbar_arrive(smem_u32(&full[c % S]));
+    uint32_t least = issued_s[0], most = issued_s[0];
+    for (int k = 1; k < 2 * CG; ++k) {
+      least = min(least, issued_s[k]);
+      most = max(most, issued_s[k]);
+    }
+    for (uint32_t c = least; c < most; ++c)
+      for (int k = 0; k < 2 * CG; ++k)
+        if (issued_s[k] <= c) mbar_arrive(smem_u32(&full[c % S]));
     for (uint32_t c = most > S ? most - S : 0; c < most; ++c)
       mbar_drain(smem_u32(&full[c % S]), (c / S) & 1u);
   }
@@ -599,33 +717,26 @@ cudaError_t run(const Maps& maps, const MuonNs& g, int64_t tiles, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, ns_kernel<CG, BN>, maps, g);
 }
 
-int64_t most_tiles(const MuonNs& g, int side) {
-  const int64_t tm = (g.rows + side - 1) / side, tn = (g.cols + side - 1) / side;
-  return tm * tn * g.batch;
-}
-
 }  // namespace
 
-cudaError_t muon_launch_ns(const MuonStack& m, const MuonNs& g, cudaStream_t st) {
+cudaError_t muon_launch_ns(const MuonNs& g, int bn, cudaStream_t st) {
   Maps maps;
   const int s = std::min(g.rows, g.cols);
-  for (int store = 0; store < 2; ++store) {
-    const int rows = store ? 32 : 64;
-    CUtensorMap* x = store ? maps.store_x : maps.load_x;
-    for (int k = 0; k < 2; ++k) {
-      const cudaError_t e = make_map({m.x[k], g.rows, g.cols, m.ld}, g.batch, rows, &x[k]);
-      if (e != cudaSuccess) return e;
-    }
-    cudaError_t e = make_map({m.a, s, s, m.lds}, g.batch, rows, store ? &maps.store_a : &maps.load_a);
-    if (e == cudaSuccess)
-      e = make_map({m.p, s, s, m.lds}, g.batch, rows, store ? &maps.store_p : &maps.load_p);
+  const Operand operands[4] = {{g.x[0], g.rows, g.cols, g.ld},
+                               {g.x[1], g.rows, g.cols, g.ld},
+                               {g.a, s, s, g.lds},
+                               {g.p, s, s, g.lds}};
+  for (int k = 0; k < 4; ++k) {
+    cudaError_t e = make_map(operands[k], g.batch, 128, &maps.rows[k]);
+    if (e == cudaSuccess) e = make_map(operands[k], g.batch, 64, &maps.cols[k]);
+    if (e == cudaSuccess) e = make_map(operands[k], g.batch, 32, &maps.store[k]);
     if (e != cudaSuccess) return e;
   }
-  // 256-wide tiles on CTA pairs halve the operand traffic; below one tile per
-  // pair the 128-wide ones keep more SMs busy.
-  const int64_t wide = most_tiles(g, 256);
-  if (wide >= 74) return run<2, 256>(maps, g, wide, st);
-  return run<1, 128>(maps, g, most_tiles(g, 128), st);
+  // No CTA is without work in the product that has most items.
+  const int64_t sym = (int64_t)((s + bn - 1) / bn) * ((s + bn - 1) / bn + 1) / 2 * g.split;
+  const int64_t upd = (int64_t)((g.rows + bn - 1) / bn) * ((g.cols + bn - 1) / bn);
+  const int64_t most = std::max(sym, upd) * g.batch;
+  return bn == 256 ? run<2, 256>(maps, g, most, st) : run<1, 128>(maps, g, most, st);
 }
 
 }  // namespace mua

@@ -67,6 +67,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
   }
   return true;
 }
+// The same for a converged warp: one answer for all lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit,
+                                               volatile uint32_t* stop) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return true;
+  const bool ok = mbar_wait(bar, parity, limit, stop);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
 // A wait for work in flight that other roles' giving up does not end.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
   uint64_t t0 = 0;
@@ -101,11 +108,6 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, 
                ::"l"(map), "r"(src), "r"(x), "r"(y), "r"(z)
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// At most N stores of this thread still read their shared memory.
-template <int N>
-__device__ __forceinline__ void tma_store_read_wait() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void tma_store_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
