@@ -18,8 +18,10 @@
 // 12) or 128 x 128 on one CTA when the 256-wide tiles would be too few for the
 // SMs. Per CTA: warps 0 and 10 stream 64-deep slices of the operands A and B
 // into a ring of 128-byte swizzled shared tiles (TMA), warp 1 issues the MMAs,
-// warps 2..9 turn finished accumulators into output while the next tile's MMAs
-// run into the other half of TMEM. The instructions between two slices' MMAs are
+// warps 2..9 turn finished accumulators into a tile in shared memory while the
+// next tile's MMAs run into the other half of TMEM, and warp 11 moves that tile
+// out (the addend of P in before), waits for it to be in memory and counts it,
+// so that nothing else stands still for it. The instructions between two slices' MMAs are
 // what bounds the rate next to the tensor cores (256 cycles of MMA a slice on
 // 128 x 128, 512 on 256 x 256): hence a warp for each operand, one copy for an
 // operand whose rows are contiguous in depth, and majors fixed per item.
@@ -35,21 +37,22 @@ namespace mua {
 namespace {
 
 constexpr int kEpilogueWarps = 8;            // two for each quarter of the TMEM lanes
-constexpr int kThreads = 96 + 32 * kEpilogueWarps;
+constexpr int kThreads = 32 * (4 + kEpilogueWarps);
+constexpr int kProducerB = 2 + kEpilogueWarps, kPorter = kProducerB + 1;  // warps
 constexpr int kOperandBytes = 16384;         // 128 rows of an operand, 64 deep
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kChunkBytes = 4096;            // 32 rows x 64 fp16 columns of output
+constexpr int kChunkBytes = 16384;           // 128 rows x 64 fp16 columns of output
 template <int BN>
 struct Ring {
-  static constexpr int chunks = BN / 128;    // an epilogue warp's share of a tile
+  static constexpr int chunks = BN / 128;    // of each half of a tile's columns
   static constexpr int stages = BN == 256 ? 5 : 6;
   static constexpr int smem =
-      stages * kStageBytes + kEpilogueWarps * chunks * kChunkBytes + 1024;  // + alignment
+      stages * kStageBytes + 2 * chunks * kChunkBytes + 1024;  // + alignment
 };
 struct Maps {
   // X of even and odd steps, A, P: boxes of 64 columns by 128 rows (an operand's
-  // rows), 64 rows (its columns) and 32 rows (the epilogue's copies).
-  CUtensorMap rows[4], cols[4], store[4];
+  // rows, and the output) and by 64 rows (an operand's columns).
+  CUtensorMap rows[4], cols[4];
 };
 
 // Tiles of one matrix in a symmetric product (the lower block triangle) and in
@@ -73,7 +76,7 @@ __device__ __forceinline__ Tiles tiles_of(const MuonNs& g) {
   return t;
 }
 
-// Work item w of the launch, in the order (step, product, matrix, tile): tile
+// Work items of the launch, in the order (step, product, matrix, tile): tile
 // (i, j) of a product of matrix z over k-slices kb0 .. kb1 - 1, which needs
 // `before` finished items of z. The triangle is walked row by row; the update
 // walks the short side's tiles first, so that tiles in flight share their slice
@@ -86,78 +89,105 @@ struct Item {
   uint32_t before;
   bool last;
 };
-struct Counts {  // items of one matrix in a step
-  uint32_t gram, reduce, poly, update, step;
+// n / d by the reciprocal ceil(2^32 / d): at most one too large for n < 2^31.
+struct Divisor {
+  uint32_t d, r;
+  __device__ __forceinline__ explicit Divisor(uint32_t x)
+      : d(x), r(x > 1 ? 0xFFFFFFFFu / x + 1u : 0u) {}
+  __device__ __forceinline__ uint32_t divide(uint32_t n) const {
+    if (d <= 1) return n;
+    const uint32_t q = __umulhi(n, r);
+    return q * d > n ? q - 1 : q;
+  }
 };
-__device__ __forceinline__ Counts counts_of(const MuonNs& g, const Tiles& T) {
-  Counts c;
-  c.gram = (uint32_t)(T.sym * g.split);
-  c.reduce = g.split > 1 ? (uint32_t)(T.sym * g.reduce) : 0u;
-  c.poly = (uint32_t)T.sym;
-  c.update = (uint32_t)T.upd;
-  c.step = c.gram + c.reduce + c.poly + c.update;
-  return c;
-}
-__device__ __forceinline__ Item item_of(const MuonNs& g, const Tiles& T, const Counts& C,
-                                        uint32_t w) {
-  Item it;
-  const uint32_t batch = (uint32_t)g.batch;
-  it.step = (int)(w / (C.step * batch));
-  uint32_t r = w - (uint32_t)it.step * C.step * batch, per = C.gram;
-  it.before = (uint32_t)it.step * C.step;
-  it.kind = kGram;
-  if (r >= per * batch) {
-    r -= per * batch;
-    it.before += per;
-    per = C.reduce;
-    it.kind = kReduce;
-    if (r >= per * batch) {
-      r -= per * batch;
-      it.before += per;
-      per = C.poly;
-      it.kind = kPoly;
-      if (r >= per * batch) {
-        r -= per * batch;
-        it.before += per;
-        per = C.update;
-        it.kind = kUpdate;
+// This CTA's (or pair's) items, one after another.
+template <int BN>
+struct Walk {
+  const MuonNs& g;
+  Tiles T;
+  uint32_t per[4], all[4], stride, left;  // items of a matrix, of a product; place in it
+  Divisor by_sym, by_upd, by_gram, by_reduce, by_split, by_share, by_short;
+  int kind = 0, step = 0;
+  __device__ __forceinline__ Walk(const MuonNs& g_, uint32_t first, uint32_t stride_)
+      : g(g_), T(tiles_of<BN>(g_)), stride(stride_), left(first), by_sym((uint32_t)T.sym),
+        by_upd((uint32_t)T.upd), by_gram((uint32_t)(T.sym * g_.split)),
+        by_reduce((uint32_t)(T.sym * g_.reduce)), by_split((uint32_t)g_.split),
+        by_share((uint32_t)g_.reduce),
+        by_short((uint32_t)(g_.rows <= g_.cols ? T.um : T.un)) {
+    per[kGram] = (uint32_t)(T.sym * g.split);
+    per[kReduce] = g.split > 1 ? (uint32_t)(T.sym * g.reduce) : 0u;
+    per[kPoly] = (uint32_t)T.sym;
+    per[kUpdate] = (uint32_t)T.upd;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) all[k] = per[k] * (uint32_t)g.batch;
+    settle();
+  }
+  __device__ __forceinline__ void settle() {
+    while (step < g.steps) {
+      const uint32_t n = kind == kGram ? all[0] : (kind == kReduce ? all[1]
+                                                                   : (kind == kPoly ? all[2] : all[3]));
+      if (left < n) break;
+      left -= n;
+      if (++kind == 4) {
+        kind = 0;
+        ++step;
       }
     }
   }
-  it.z = (int)(r / per);
-  int t = (int)(r - (uint32_t)it.z * per);
-  it.share = 0;
-  it.kb0 = 0;
-  it.kb1 = T.update;
-  if (it.kind == kGram) {
-    const int tile = t / g.split;
-    it.share = t - tile * g.split;
-    t = tile;
-    it.kb0 = it.share * T.gram / g.split;
-    it.kb1 = (it.share + 1) * T.gram / g.split;
-  } else if (it.kind == kReduce) {
-    const int tile = t / g.reduce;
-    it.share = t - tile * g.reduce;
-    t = tile;
+  __device__ __forceinline__ bool more() const { return step < g.steps; }
+  __device__ __forceinline__ void advance() {
+    left += stride;
+    settle();
   }
-  it.tile = t;
-  it.last = it.kind == kUpdate && it.step == g.steps - 1;
-  if (it.kind == kUpdate) {
-    if (g.rows <= g.cols) {
-      it.j = t / T.um;
-      it.i = t - it.j * T.um;
+  __device__ __forceinline__ Item item() const {
+    Item it;
+    it.step = step;
+    it.kind = kind;
+    it.before = (uint32_t)step * (per[0] + per[1] + per[2] + per[3]);
+    it.share = 0;
+    it.kb0 = 0;
+    it.kb1 = T.update;
+    it.last = false;
+    uint32_t z, t;
+    if (kind == kUpdate) {
+      it.before += per[0] + per[1] + per[2];
+      it.last = step == g.steps - 1;
+      z = by_upd.divide(left);
+      t = left - z * per[3];
+      const uint32_t q = by_short.divide(t), r = t - q * by_short.d;
+      it.i = (int)(g.rows <= g.cols ? r : q);
+      it.j = (int)(g.rows <= g.cols ? q : r);
     } else {
-      it.i = t / T.un;
-      it.j = t - it.i * T.un;
+      if (kind == kPoly) {
+        it.before += per[0] + per[1];
+        z = by_sym.divide(left);
+        t = left - z * per[2];
+      } else if (kind == kReduce) {
+        it.before += per[0];
+        z = by_reduce.divide(left);
+        t = left - z * per[1];
+        const uint32_t q = by_share.divide(t);
+        it.share = (int)(t - q * by_share.d);
+        t = q;
+      } else {
+        z = by_gram.divide(left);
+        t = left - z * per[0];
+        const uint32_t q = by_split.divide(t);
+        it.share = (int)(t - q * by_split.d);
+        t = q;
+        it.kb0 = g.split > 1 ? it.share * T.gram / g.split : 0;
+        it.kb1 = g.split > 1 ? (it.share + 1) * T.gram / g.split : T.gram;
+      }
+      it.i = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+      while (it.i * (it.i + 1) / 2 > (int)t) --it.i;
+      while ((it.i + 1) * (it.i + 2) / 2 <= (int)t) ++it.i;
+      it.j = (int)t - it.i * (it.i + 1) / 2;
     }
-  } else {
-    it.i = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-    while (it.i * (it.i + 1) / 2 > t) --it.i;
-    while ((it.i + 1) * (it.i + 2) / 2 <= t) ++it.i;
-    it.j = t - it.i * (it.i + 1) / 2;
+    it.z = (int)z;
+    it.tile = (int)t;
+    return it;
   }
-  return it;
-}
+};
 // First k-slice of an item whose operand (A or B) is read with its M / N index
 // contiguous. X has one major per product; A and P (symmetric) are read from
 // below the diagonal, as rows up to the diagonal block and columns behind it.
@@ -170,8 +200,8 @@ __device__ __forceinline__ int first_mn(const MuonNs& g, const Item& it, bool a)
   return tall ? never : 0;
 }
 
-// Waits until matrix z has `tiles` finished tiles (every epilogue warp of a
-// tile counts one). Items are taken in order by CTAs that are all resident, and
+// Waits until matrix z has `want` finished items (every CTA of an item counts
+// one). Items are taken in order by CTAs that are all resident, and
 // need earlier items only, so the wait ends.
 __device__ __forceinline__ bool matrix_wait(const MuonNs& g, int z, uint32_t want,
                                             volatile uint32_t* stop) {
@@ -192,7 +222,7 @@ __device__ __forceinline__ bool matrix_wait(const MuonNs& g, int z, uint32_t wan
   }
 }
 
-// This warp's part of an item is in memory: count it.
+// This CTA's part of an item is in memory: count it.
 __device__ __forceinline__ void count_item(const MuonNs& g, int z) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(g.counters + z) : "memory");
 }
@@ -226,6 +256,31 @@ __device__ __forceinline__ void reduce_rows(const MuonNs& g, const Tiles& T, con
   }
 }
 
+// 64 columns of a warp's rows of P, in place of A's in the output tile.
+template <bool DIAGONAL>
+__device__ __forceinline__ void poly_chunk(uint32_t tile, int lane, const uint32_t (&v)[2][32],
+                                           float alpha, float mid, float diag, int diagonal) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint32_t at = chunk_address(tile, lane, q);
+    const uint4 a = ld_shared(at);
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
+      float x0 = fmaf(y.x, mid, __uint_as_float(v[q >> 2][(8 * q + 2 * e) & 31]) * alpha);
+      float x1 = fmaf(y.y, mid, __uint_as_float(v[q >> 2][(8 * q + 2 * e + 1) & 31]) * alpha);
+      if constexpr (DIAGONAL) {
+        if (8 * q + 2 * e == diagonal) x0 += diag;
+        if (8 * q + 2 * e + 1 == diagonal) x1 += diag;
+      }
+      h[e] = pack_f16(x0, x1);
+    }
+    st_shared(at, h[0], h[1], h[2], h[3]);
+  }
+}
+
 template <int CG, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
 ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
@@ -234,16 +289,14 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
   constexpr uint32_t kTmemCols = 2 * BN;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drained;
-  __shared__ __align__(8) uint64_t addend_full[kEpilogueWarps][kChunks];
+  // The output tile in shared memory: all parts written; free again; P's addend there.
+  __shared__ __align__(8) uint64_t staged, room, addend;
   __shared__ uint32_t tmem_base_s, stop;
   __shared__ uint32_t issued_s[4];  // copies of A and of B, of this CTA and the pair's other
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? (blockIdx.x & 1u) : 0u;
   const uint32_t first = blockIdx.x / CG, stride = gridDim.x / CG;
-  const Tiles tiles = tiles_of<BN>(g);
-  const Counts counts = counts_of(g, tiles);
-  const uint32_t items = counts.step * (uint32_t)(g.batch * g.steps);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -254,8 +307,9 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
       mbar_init(smem_u32(&acc_full[a]), 1);
       mbar_init(smem_u32(&acc_empty[a]), kEpilogueWarps * CG);
     }
-    for (int w = 0; w < kEpilogueWarps; ++w)
-      for (int c = 0; c < kChunks; ++c) mbar_init(smem_u32(&addend_full[w][c]), 1);
+    mbar_init(smem_u32(&staged), kEpilogueWarps);
+    mbar_init(smem_u32(&room), 1);
+    mbar_init(smem_u32(&addend), 1);
     mbar_init(smem_u32(&drained), 1);
     stop = 0;
     for (int k = 0; k < 4; ++k) issued_s[k] = 0;
@@ -285,16 +339,17 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
 
   // The producing and issuing warps run their loops converged; an elected lane
   // issues.
-  if (warp == 0 || warp == kThreads / 32 - 1) {
+  const uint32_t tile_base = ring + S * kStageBytes;
+  if (warp == 0 || warp == kProducerB) {
     const bool is_a = warp == 0;
     const uint32_t lead = CG == 2 && rank != 0 ? peer_address(smem_u32(&full[0]), 0) : 0;
     uint32_t issued = 0, s = 0, turn = 1;
     bool ok = true;
     int ready_z = -1;
     uint32_t ready = 0;
-    for (uint32_t w = first; ok && w < items; w += stride) {
-      const Item it = item_of(g, tiles, counts, w);
-      if (it.kind == kReduce) continue;
+    for (Walk<BN> walk(g, first, stride); ok && walk.more(); walk.advance()) {
+      if (walk.kind == kReduce) continue;
+      const Item it = walk.item();
       const bool tall = g.rows > g.cols;
       const int mn_from = first_mn<BN>(g, it, is_a);
       const int which = it.kind == kGram || (it.kind == kUpdate && is_a == tall)
@@ -304,7 +359,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
       const int m0 = is_a ? it.i * BN + (int)rank * 128          // this CTA's rows of A
                           : it.j * BN + (int)rank * (BN / CG);   // and of B
       if (it.z != ready_z || it.before != ready) {
-        ok = matrix_wait(g, it.z, it.before * (CG * kEpilogueWarps), stop_v);
+        ok = matrix_wait(g, it.z, it.before * CG, stop_v);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         fence_async_global();
@@ -350,9 +405,9 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
     if (rank == 0) {
       uint32_t n = 0, s = 0, turn = 0;
       bool ok = true;
-      for (uint32_t w = first; ok && w < items; w += stride) {
-        const Item it = item_of(g, tiles, counts, w);
-        if (it.kind == kReduce) continue;
+      for (Walk<BN> walk(g, first, stride); ok && walk.more(); walk.advance()) {
+        if (walk.kind == kReduce) continue;
+        const Item it = walk.item();
         const uint32_t acc = n & 1u;
         ok = mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1u) ^ 1u, g.wait_ns, stop_v);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -397,114 +452,138 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
         mbar_drain(smem_u32(&drained), 0);
       }
     }
+  } else if (warp == kPorter) {
+    const bool elected = elect_one();
+    uint32_t done = 0, addends = 0;  // items, and those with an addend
+    bool ok = true;
+    for (Walk<BN> walk(g, first, stride); ok && walk.more(); walk.advance()) {
+      const Item it = walk.item();
+      if (it.last) break;
+      const int M = it.kind == kUpdate ? g.rows : min(g.rows, g.cols);
+      const int N = it.kind == kUpdate ? g.cols : M;
+      const int row0 = it.i * BN + (int)rank * 128;
+      // 64-column chunks of the tile that hold output, from its first column on.
+      const int chunks = row0 < M ? min(BN / 64, (N - it.j * BN + 63) / 64) : 0;
+      if (it.kind == kPoly) {
+        ok = matrix_wait(g, it.z, it.before * CG, stop_v);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        if (elected) {
+          fence_async_global();
+          if (chunks > 0)
+            mbar_expect(smem_u32(&addend), (uint32_t)chunks * kChunkBytes);
+          else
+            mbar_arrive(smem_u32(&addend));
+          for (int c = 0; c < chunks; ++c)
+            tma_load<1>(tile_base + c * kChunkBytes, &maps.rows[2], smem_u32(&addend),
+                        it.j * BN + 64 * c, row0, it.z);
+        }
+        __syncwarp();
+        ++addends;
+      }
+      ok = mbar_wait_warp(smem_u32(&staged), done & 1u, g.wait_ns, stop_v);
+      if (!ok) break;
+      if (elected) {
+        if (it.kind != kReduce && !(it.kind == kGram && g.split > 1)) {
+          const CUtensorMap* out =
+              &maps.rows[it.kind == kGram ? 2 : (it.kind == kPoly ? 3 : (it.step & 1) ^ 1)];
+          for (int c = 0; c < chunks; ++c)
+            tma_store(out, tile_base + c * kChunkBytes, it.j * BN + 64 * c, row0, it.z);
+          tma_store_commit();
+          tma_store_read_wait();
+          mbar_arrive(smem_u32(&room));
+          tma_store_wait_all();
+        } else {
+          mbar_arrive(smem_u32(&room));
+        }
+        count_item(g, it.z);
+      }
+      __syncwarp();
+      ++done;
+    }
+    if (addends > 0) mbar_drain(smem_u32(&addend), (addends - 1) & 1u);
   } else {
-    const int quarter = warp & 3;     // the TMEM lanes this warp may read
+    const int quarter = warp & 3;      // the TMEM lanes this warp may read
     const int side = (warp - 2) >> 2;  // its half of the tile's columns
-    const uint32_t stage = ring + S * kStageBytes + (warp - 2) * kChunks * kChunkBytes;
-    uint32_t n = 0;
-    uint32_t asked = 0, parity = 0;  // per chunk: an addend copy in flight, its barrier's phase
+    // Its 32 rows of the half's chunks in the output tile.
+    const uint32_t stage = tile_base + side * kChunks * kChunkBytes + quarter * 4096;
+    uint32_t n = 0, out_items = 0, addends = 0;  // items with MMAs, moved out, with an addend
     int ready_z = -1;
     uint32_t ready = 0;
     bool ok = true;
-    for (uint32_t w = first; ok && w < items; w += stride) {
-      const Item it = item_of(g, tiles, counts, w);
+    for (Walk<BN> walk(g, first, stride); ok && walk.more(); walk.advance()) {
+      const Item it = walk.item();
       const int M = it.kind == kUpdate ? g.rows : min(g.rows, g.cols);
       const int N = it.kind == kUpdate ? g.cols : M;
       const int row0 = it.i * BN + (int)rank * 128 + quarter * 32;
       const int col0 = it.j * BN + side * (BN / 2);
       const int chunks = row0 < M ? max(0, min(kChunks, (N - col0 + 63) / 64)) : 0;
-      if ((it.kind == kPoly && chunks > 0) || it.kind == kReduce) {
-        if (it.z != ready_z || it.before != ready) {
-          ok = matrix_wait(g, it.z, it.before * (CG * kEpilogueWarps), stop_v);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          fence_async_global();
-          ready_z = it.z;
-          ready = it.before;
-        }
-      }
       float f = it.step == 0 && it.kind != kPoly ? g.factor[it.z] : 1.0f;
       if (it.kind <= kReduce) f *= f;
       const float alpha = f * (it.kind <= kReduce ? g.gram_alpha[it.step]
                                                   : (it.kind == kPoly ? g.poly_alpha[it.step]
                                                                       : g.update_alpha[it.step]));
       if (it.kind == kReduce) {
-        reduce_rows<CG, BN>(g, tiles, it, rank, warp - 2, lane, alpha);
+        if (it.z != ready_z || it.before != ready) {
+          ok = matrix_wait(g, it.z, it.before * CG, stop_v);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          ready_z = it.z;
+          ready = it.before;
+        }
+        reduce_rows<CG, BN>(g, walk.T, it, rank, warp - 2, lane, alpha);
+        // No warp arrives for an item before all have arrived for the last one.
+        ok = mbar_wait_warp(smem_u32(&room), (out_items & 1u) ^ 1u, g.wait_ns, stop_v);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(smem_u32(&staged));
         __syncwarp();
-        if (lane == 0) count_item(g, it.z);
+        ++out_items;
         continue;
       }
       const uint32_t acc = n & 1u;
-      if (it.kind == kPoly && chunks > 0) {
-        // The addend on its way while the MMAs run.
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          for (int c = 0; c < chunks; ++c) {
-            const uint32_t bar = smem_u32(&addend_full[warp - 2][c]);
-            mbar_expect(bar, kChunkBytes);
-            tma_load<1>(stage + c * kChunkBytes, &maps.store[2], bar, col0 + 64 * c, row0, it.z);
-          }
-        }
-        asked = (1u << chunks) - 1u;
-      }
-      ok = mbar_wait(smem_u32(&acc_full[acc]), (n >> 1) & 1u, g.wait_ns, stop_v);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      ok = mbar_wait_warp(smem_u32(&acc_full[acc]), (n >> 1) & 1u, g.wait_ns, stop_v);
       if (!ok) break;
       fence_after();
+      ok = mbar_wait_warp(smem_u32(&room), (out_items & 1u) ^ 1u, g.wait_ns, stop_v);
+      if (!ok) break;
+      if (it.kind == kPoly) {
+        ok = mbar_wait_warp(smem_u32(&addend), addends & 1u, g.wait_ns, stop_v);
+        if (!ok) break;
+        ++addends;
+      }
       const uint32_t lanes =
           tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + side * (BN / 2);
       const bool partial = it.kind == kGram && g.split > 1;
       if (!it.last && !partial) {
         const float mid = g.poly_mid[it.step], diag = g.poly_diag[it.step];
-        const CUtensorMap* out =
-            &maps.store[it.kind == kGram ? 2 : (it.kind == kPoly ? 3 : (it.step & 1) ^ 1)];
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
           const uint32_t tile = stage + c * kChunkBytes;
           uint32_t v[2][32];
           tmem_load32(lanes + 64 * c, v[0]);
           tmem_load32(lanes + 64 * c + 32, v[1]);
-          if (it.kind == kPoly) {
-            mbar_drain(smem_u32(&addend_full[warp - 2][c]), (parity >> c) & 1u);
-            asked &= ~(1u << c);
-            parity ^= 1u << c;
-          }
           tmem_load_wait();
-          const int diagonal = row0 + lane - (col0 + 64 * c);  // column of the diagonal
+          if (it.kind == kPoly) {
+            const int diagonal = row0 + lane - (col0 + 64 * c);  // column of the diagonal
+            if (row0 < col0 + 64 * c + 64 && col0 + 64 * c < row0 + 32)
+              poly_chunk<true>(tile, lane, v, alpha, mid, diag, diagonal);
+            else
+              poly_chunk<false>(tile, lane, v, alpha, mid, diag, diagonal);
+          } else {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t at = chunk_address(tile, lane, q);
-            uint32_t h[4];
-            if (it.kind == kPoly) {
-              const uint4 a = ld_shared(at);
-              const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
-                float x0 = __uint_as_float(v[q >> 2][(8 * q + 2 * e) & 31]) * alpha;
-                float x1 = __uint_as_float(v[q >> 2][(8 * q + 2 * e + 1) & 31]) * alpha;
-                x0 = fmaf(y.x, mid, x0);
-                x1 = fmaf(y.y, mid, x1);
-                if (8 * q + 2 * e == diagonal) x0 += diag;
-                if (8 * q + 2 * e + 1 == diagonal) x1 += diag;
-                h[e] = pack_f16(x0, x1);
-              }
-            } else {
+            for (int q = 0; q < 8; ++q) {
+              uint32_t h[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 h[e] = pack_f16(__uint_as_float(v[q >> 2][(8 * q + 2 * e) & 31]) * alpha,
                                 __uint_as_float(v[q >> 2][(8 * q + 2 * e + 1) & 31]) * alpha);
+              st_shared(chunk_address(tile, lane, q), h[0], h[1], h[2], h[3]);
             }
-            st_shared(at, h[0], h[1], h[2], h[3]);
           }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) tma_store(out, tile, col0 + 64 * c, row0, it.z);
         }
       } else if (partial) {
         float* out = g.partials +
-                     (((int64_t)it.z * tiles.sym + it.tile) * g.split + it.share) * (BN * BN) +
+                     (((int64_t)it.z * walk.T.sym + it.tile) * g.split + it.share) * (BN * BN) +
                      (int)(rank * 128 + quarter * 32) * BN + side * (BN / 2);
 #pragma unroll 1
         for (int c = 0; c < 2 * chunks; ++c) {
@@ -559,23 +638,19 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
         }
       }
       fence_before();
+      fence_async_shared();
       __syncwarp();
       if (lane == 0) {
         if (CG == 2 && rank != 0)
           mbar_arrive_cluster(peer_address(smem_u32(&acc_empty[acc]), 0));
         else
           mbar_arrive(smem_u32(&acc_empty[acc]));
-        if (!it.last) {
-          tma_store_wait_all();
-          count_item(g, it.z);
-        }
+        if (!it.last) mbar_arrive(smem_u32(&staged));
       }
       __syncwarp();
       ++n;
+      if (!it.last) ++out_items;
     }
-    for (int c = 0; c < kChunks; ++c)
-      if (asked >> c & 1u)
-        mbar_drain(smem_u32(&addend_full[warp - 2][c]), (parity >> c) & 1u);
   }
   __syncwarp();
   fence_before();
@@ -729,7 +804,6 @@ cudaError_t muon_launch_ns(const MuonNs& g, int bn, cudaStream_t st) {
   for (int k = 0; k < 4; ++k) {
     cudaError_t e = make_map(operands[k], g.batch, 128, &maps.rows[k]);
     if (e == cudaSuccess) e = make_map(operands[k], g.batch, 64, &maps.cols[k]);
-    if (e == cudaSuccess) e = make_map(operands[k], g.batch, 32, &maps.store[k]);
     if (e != cudaSuccess) return e;
   }
   // No CTA is without work in the product that has most items.
