@@ -8,11 +8,13 @@
 // read twice, and U is formed from the unrounded m' in the same pass.
 #include "muon_quant.cuh"
 
+#include <algorithm>
+
 namespace mua {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kNormUnroll = 4;
+constexpr int kNormUnroll = 4, kLoadUnroll = 2;
 constexpr int kUnroll = 2;                             // blocks per half-warp
 constexpr int kChunkBlocks = kThreads / 16 * kUnroll;  // 32 blocks (4096 values) per CTA
 
@@ -25,7 +27,8 @@ __device__ __forceinline__ void release_next() {
 
 // ---------------------------------------------------------------- kernels
 
-// Grid: splits x count CTAs, a CTA takes 32 consecutive blocks of one matrix.
+// Grid: splits x count CTAs; a CTA takes every splits-th run of 16 blocks of one
+// matrix, the next run's loads in flight while it works on one.
 // OUT: 0 fp32, 1 bf16 (contiguous), 2 fp16 X_0 with row stride ld.
 template <int BITS, int G, int OUT>
 __global__ void __launch_bounds__(kThreads, 4)
@@ -34,29 +37,32 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
                 float eps, int e0, void* X, float* factor, uint32_t* counters, int splits) {
   wait_previous();
   release_next();
+  constexpr int kRun = kThreads / 16;
   const int mat = blockIdx.x / splits, split = blockIdx.x - mat * splits;
   const int64_t n = (int64_t)s.rows * s.cols;
   const int half = threadIdx.x >> 4, sub = threadIdx.x & 15;
-  const int es = G == kBf16 ? 2 : 4;
-  const void* gm = static_cast<const uint8_t*>(g) + mat * n * es;
+  const void* gm = static_cast<const uint8_t*>(g) + mat * n * (G == kBf16 ? 2 : 4);
   const bool vec = aligned16(gm);
-  const int64_t first = (int64_t)split * kChunkBlocks + half;
   const int64_t base = mat * Q.bpm;
+  constexpr int os = OUT == kBf16 ? 2 : 4;
+  uint8_t* om = static_cast<uint8_t*>(out) + mat * n * os;
+  const bool out_vec = OUT != 2 && aligned16(om);
+  const int64_t step = (int64_t)splits * kRun;
 
-  uint64_t gv[kUnroll][4];
-  uint2 codes[kUnroll];
-  float scale[kUnroll];
-#pragma unroll
-  for (int k = 0; k < kUnroll; ++k) {
-    const int64_t b = first + k * (kThreads / 16);
-    codes[k] = make_uint2(0u, 0u);
-    scale[k] = 0.0f;
+  uint64_t next_g[4];
+  uint2 next_codes;
+  float next_scale;
+  auto fetch = [&](int64_t b) {
+    next_codes = make_uint2(0u, 0u);
+    next_scale = 0.0f;
     if (b < Q.bpm) {
-      codes[k] = load_codes<BITS>(Q.codes, base + b, sub);
-      scale[k] = Q.scales[base + b];
+      next_codes = load_codes<BITS>(Q.codes, base + b, sub);
+      next_scale = Q.scales[base + b];
     }
-    load8<G>(gm, b * kMuonBlock + 8 * sub, n, vec, gv[k]);
-  }
+    load8<G>(gm, b * kMuonBlock + 8 * sub, n, vec, next_g);
+  };
+  int64_t run = (int64_t)split * kRun;
+  fetch(run + half);
   NormScale ns;
   if constexpr (OUT == 2) {
     ns = norm_scale(partials + (int64_t)mat * s.parts, s.parts, eps, e0);
@@ -66,12 +72,12 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
     }
   }
   bool bad = false;
-#pragma unroll
-  for (int k = 0; k < kUnroll; ++k) {
-    const int64_t b = first + k * (kThreads / 16);
+  for (; run < Q.bpm; run += step) {
+    const int64_t b = run + half;
     uint64_t q[4], m[4], u[4];
-    unpack8<BITS>(codes[k], q);
-    new_momentum(q, scale[k], gv[k], beta, nesterov, m, u);
+    unpack8<BITS>(next_codes, q);
+    new_momentum(q, next_scale, next_g, beta, nesterov, m, u);
+    if (run + step < Q.bpm) fetch(b + step);
     const int64_t i = b * kMuonBlock + 8 * sub;
     const int left = left_of(i, n);
     float new_scale;
@@ -102,9 +108,7 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
           }
         }
       } else {
-        const int os = OUT == kBf16 ? 2 : 4;
-        uint8_t* om = static_cast<uint8_t*>(out) + mat * n * os;
-        store8<OUT>(om, i, n, aligned16(om), u);
+        store8<OUT>(om, i, n, out_vec, u);
       }
     }
   }
@@ -204,13 +208,21 @@ load_kernel(MuonShape s, MuonView x, const double* partials, float eps, int e0, 
     counters[mat] = 0;
   }
   __half* out = static_cast<__half*>(X) + (int64_t)mat * s.rows * s.ld;
-  for (uint64_t q = (uint64_t)split * kThreads + threadIdx.x; q < groups;
-       q += (uint64_t)splits * kThreads) {
-    const uint32_t row = (uint32_t)q / per_row, col = 8 * ((uint32_t)q - row * per_row);
-    uint64_t v[4];
-    load8<T>(xm + (int64_t)row * x.row_stride * es, col, s.cols, vec, v);
-    *reinterpret_cast<uint4*>(out + (int64_t)row * s.ld + col) =
-        scaled_f16(v, ns.first, ns.second);
+  const uint64_t stride = (uint64_t)splits * kThreads;
+  for (uint64_t q0 = (uint64_t)split * kThreads + threadIdx.x; q0 < groups;
+       q0 += kLoadUnroll * stride) {
+    uint64_t v[kLoadUnroll][4];
+    uint4* to[kLoadUnroll];
+#pragma unroll
+    for (int k = 0; k < kLoadUnroll; ++k) {
+      const uint64_t q = q0 + k * stride;
+      const uint32_t row = (uint32_t)q / per_row, col = 8 * ((uint32_t)q - row * per_row);
+      to[k] = q < groups ? reinterpret_cast<uint4*>(out + (int64_t)row * s.ld + col) : nullptr;
+      load8<T>(xm + (int64_t)row * x.row_stride * es, col, q < groups ? s.cols : 0, vec, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kLoadUnroll; ++k)
+      if (to[k]) *to[k] = scaled_f16(v[k], ns.first, ns.second);
   }
 }
 
@@ -301,6 +313,13 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, cudaStream_t st, bool ove
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// CTAs a matrix is split over: about eight for each SM of a B200 in all, as each
+// begins with the norm's sum, and none without work.
+int splits_for(int count, int64_t work, int64_t per_cta) {
+  const int64_t most = (work + per_cta - 1) / per_cta;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, (8 * 148 + count - 1) / count));
+}
+
 int64_t chunk_splits(const MuonQuant& q) { return (q.bpm + kChunkBlocks - 1) / kChunkBlocks; }
 
 }  // namespace
@@ -315,9 +334,7 @@ cudaError_t muon_launch_norm(const MuonShape& s, const MuonView& x, double* part
 cudaError_t muon_launch_load(const MuonShape& s, const MuonView& x, const double* partials,
                              float eps, int e0, void* X, float* factor, uint32_t* counters,
                              cudaStream_t st) {
-  // Two 16-byte groups per thread.
-  const int64_t groups = (int64_t)s.rows * (s.ld / 8);
-  const int splits = (int)((groups + 2 * kThreads - 1) / (2 * kThreads));
+  const int splits = splits_for(s.count, (int64_t)s.rows * (s.ld / 8), kLoadUnroll * kThreads);
   const int64_t grid = (int64_t)s.count * splits;
   auto k = x.type == kBf16 ? load_kernel<kBf16> : load_kernel<kF32>;
   return launch(k, grid, st, true, s, x, partials, eps, e0, X, factor, counters, splits);
@@ -345,12 +362,12 @@ cudaError_t muon_launch_momentum(const MuonShape& s, const MuonQuant& q, const v
                                  float beta, int nesterov, const MuonRandom& rnd, void* out,
                                  int out_type, const double* partials, float eps, int e0, void* X,
                                  float* factor, uint32_t* counters, cudaStream_t st) {
-  const int64_t splits = chunk_splits(q);
+  const int splits = splits_for(s.count, q.bpm, kThreads / 16);
   auto k = X ? pick_momentum<2>(q.bits, g_type)
              : (out_type == kBf16 ? pick_momentum<1>(q.bits, g_type)
                                   : pick_momentum<0>(q.bits, g_type));
-  return launch(k, splits * s.count, st, X != nullptr, s, q, g, beta, nesterov, rnd, out, partials,
-                eps, e0, X, factor, counters, (int)splits);
+  return launch(k, (int64_t)splits * s.count, st, X != nullptr, s, q, g, beta, nesterov, rnd, out,
+                partials, eps, e0, X, factor, counters, splits);
 }
 
 cudaError_t muon_launch_read(const MuonShape& s, const MuonQuant& q, void* out, int out_type,

@@ -256,7 +256,19 @@ __device__ __forceinline__ int left_of(int64_t i, int64_t n) {
   return (int)(i + 8 <= n ? 8 : (i < n ? n - i : 0));
 }
 
+__device__ __forceinline__ uint64_t f2_fma_rn(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// Sum of 8 squares: in fp32 (a relative error of 2^-22 at most) where that holds
+// it, else in fp64, whose range holds every square.
 __device__ __forceinline__ double sum_squares(const uint64_t (&v)[4]) {
+  uint64_t t = f2_mul_rn(v[0], v[0]);
+#pragma unroll
+  for (int e = 1; e < 4; ++e) t = f2_fma_rn(v[e], v[e], t);
+  const float f = f2_lo(t) + f2_hi(t);
+  if (f > 1e-20f && f < 1e30f) return (double)f;
   double s = 0.0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
