@@ -24,7 +24,6 @@ namespace mua {
 
 constexpr int kMuonBlock = 128;          // values per quantization scale
 constexpr int kMuonMaxSteps = 16;
-constexpr int kMuonMaxParts = 256;       // partial sums of one matrix's norm
 constexpr int kMuonHdrStatus = 4;        // header word, as in the MicroAdam state
 constexpr uint32_t kMuonNonFinite = 1u;
 constexpr uint32_t kMuonTimeout = 2u;

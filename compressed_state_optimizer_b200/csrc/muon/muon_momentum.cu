@@ -47,22 +47,27 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
   constexpr int os = OUT == kBf16 ? 2 : 4;
   uint8_t* om = static_cast<uint8_t*>(out) + mat * n * os;
   const bool out_vec = OUT != 2 && aligned16(om);
-  const int64_t step = (int64_t)splits * kRun;
 
+  // This lane's place in the run: pointers, which advance by a step, and the
+  // index in the matrix (below 2^31).
+  const uint32_t blocks = (uint32_t)Q.bpm, step = (uint32_t)splits * kRun;
+  uint32_t b = (uint32_t)split * kRun + half;
+  uint8_t* codes = Q.codes + ((base + b) * kMuonBlock + 8 * sub) * BITS / 8;
+  float* scales = Q.scales + base + b;
   uint64_t next_g[4];
   uint2 next_codes;
   float next_scale;
-  auto fetch = [&](int64_t b) {
+  auto fetch = [&](uint32_t at, const uint8_t* c, const float* sc) {
     next_codes = make_uint2(0u, 0u);
     next_scale = 0.0f;
-    if (b < Q.bpm) {
-      next_codes = load_codes<BITS>(Q.codes, base + b, sub);
-      next_scale = Q.scales[base + b];
+    if (at < blocks) {
+      next_codes = load_codes<BITS>(c);
+      next_scale = *sc;
     }
-    load8<G>(gm, b * kMuonBlock + 8 * sub, n, vec, next_g);
+    load8<G>(gm, (int64_t)at * kMuonBlock + 8 * sub, n, vec, next_g);
   };
-  int64_t run = (int64_t)split * kRun;
-  fetch(run + half);
+  fetch(b, codes, scales);
+  uint64_t counter = (uint64_t)(rnd.base + (base + b) * kMuonBlock) / 8 + sub;
   NormScale ns;
   if constexpr (OUT == 2) {
     ns = norm_scale(partials + (int64_t)mat * s.parts, s.parts, eps, e0);
@@ -72,21 +77,24 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
     }
   }
   bool bad = false;
-  for (; run < Q.bpm; run += step) {
-    const int64_t b = run + half;
+  for (; b - half < blocks; b += step) {
     uint64_t q[4], m[4], u[4];
     unpack8<BITS>(next_codes, q);
     new_momentum(q, next_scale, next_g, beta, nesterov, m, u);
-    if (run + step < Q.bpm) fetch(b + step);
-    const int64_t i = b * kMuonBlock + 8 * sub;
+    uint8_t* codes_now = codes;
+    float* scales_now = scales;
+    codes += (int64_t)step * (kMuonBlock * BITS / 8);
+    scales += step;
+    if (b - half + step < blocks) fetch(b + step, codes, scales);
+    const int64_t i = (int64_t)b * kMuonBlock + 8 * sub;
     const int left = left_of(i, n);
     float new_scale;
     uint32_t c[8];
-    quantize_block<BITS>(m, left, (uint64_t)(rnd.base + (base + b) * kMuonBlock) / 8 + sub, rnd,
-                         new_scale, c, bad);
-    if (b < Q.bpm) {
-      store_codes<BITS>(Q.codes, base + b, sub, c);
-      if (sub == 0) Q.scales[base + b] = new_scale;
+    quantize_block<BITS>(m, left, counter, rnd, new_scale, c, bad);
+    counter += (uint64_t)step * (kMuonBlock / 8);
+    if (b < blocks) {
+      store_codes<BITS>(codes_now, c);
+      if (sub == 0) *scales_now = new_scale;
       if constexpr (OUT == 2) {
         __half* x = static_cast<__half*>(X) + (int64_t)mat * s.rows * s.ld;
         const uint4 h = scaled_f16(u, ns.first, ns.second);
@@ -130,28 +138,34 @@ direction_norm_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int n
   const int64_t base = mat * Q.bpm;
   double sum = 0.0;
   const int64_t stride = (int64_t)s.parts * (kThreads / 16);
-  for (int64_t b0 = (int64_t)part * (kThreads / 16) + half; b0 < Q.bpm; b0 += kNormUnroll * stride) {
-    uint64_t gv[kNormUnroll][4];
-    uint2 codes[kNormUnroll];
-    float scale[kNormUnroll];
-#pragma unroll
-    for (int k = 0; k < kNormUnroll; ++k) {
-      const int64_t b = b0 + k * stride;
-      codes[k] = make_uint2(0u, 0u);
-      scale[k] = 0.0f;
-      if (b < Q.bpm) {
-        codes[k] = load_codes<BITS>(Q.codes, base + b, sub);
-        scale[k] = Q.scales[base + b];
-      }
-      load8<G>(gm, b * kMuonBlock + 8 * sub, n, vec, gv[k]);
+  uint64_t gv[kNormUnroll][4];
+  uint2 codes[kNormUnroll];
+  float scale[kNormUnroll];
+  auto fetch = [&](int k, int64_t b) {
+    codes[k] = make_uint2(0u, 0u);
+    scale[k] = 0.0f;
+    if (b < Q.bpm) {
+      codes[k] = load_codes<BITS>(Q.codes, base + b, sub);
+      scale[k] = Q.scales[base + b];
     }
+    load8<G>(gm, b * kMuonBlock + 8 * sub, n, vec, gv[k]);
+  };
+  int64_t b = (int64_t)part * (kThreads / 16) + half;
 #pragma unroll
-    for (int k = 0; k < kNormUnroll; ++k) {
+  for (int k = 0; k < kNormUnroll; ++k) fetch(k, b + k * stride);
+  while (b < Q.bpm) {
+#pragma unroll
+    for (int k = 0; k < kNormUnroll; ++k) {  // a block, and the loads of one further on
       // Codes behind the last value are 0 and its gradients read as 0.
       uint64_t q[4], m[4], u[4];
       unpack8<BITS>(codes[k], q);
       new_momentum(q, scale[k], gv[k], beta, nesterov, m, u);
+      if (b + kNormUnroll * stride < Q.bpm)
+        fetch(k, b + kNormUnroll * stride);
+      else
+        codes[k] = make_uint2(0u, 0u), gv[k][0] = gv[k][1] = gv[k][2] = gv[k][3] = 0;
       sum += sum_squares(u);
+      b += stride;
     }
   }
   const double t = cta_sum<kThreads>(sum);
@@ -175,17 +189,21 @@ norm_kernel(MuonShape s, MuonView x, double* partials) {
   const uint32_t groups = per_row * (flat ? 1u : (uint32_t)s.rows);
   double sum = 0.0;
   const uint64_t stride = (uint64_t)s.parts * kThreads;
-  for (uint64_t q0 = (uint64_t)part * kThreads + threadIdx.x; q0 < groups;
-       q0 += kNormUnroll * stride) {
-    uint64_t v[kNormUnroll][4];
+  uint64_t v[kNormUnroll][4];
+  auto fetch = [&](int k, uint64_t q) {
+    const uint32_t row = (uint32_t)q / per_row, col = 8 * ((uint32_t)q - row * per_row);
+    load8<T>(xm + (int64_t)row * x.row_stride * es, col, q < groups ? cols : 0, vec, v[k]);
+  };
+  uint64_t q = (uint64_t)part * kThreads + threadIdx.x;
 #pragma unroll
-    for (int k = 0; k < kNormUnroll; ++k) {
-      const uint64_t q = q0 + k * stride;
-      const uint32_t row = (uint32_t)q / per_row, col = 8 * ((uint32_t)q - row * per_row);
-      load8<T>(xm + (int64_t)row * x.row_stride * es, col, q < groups ? cols : 0, vec, v[k]);
+  for (int k = 0; k < kNormUnroll; ++k) fetch(k, q + k * stride);
+  while (q < groups) {
+#pragma unroll
+    for (int k = 0; k < kNormUnroll; ++k) {  // a group, and the loads of one further on
+      sum += sum_squares(v[k]);
+      fetch(k, q + kNormUnroll * stride);
+      q += stride;
     }
-#pragma unroll
-    for (int k = 0; k < kNormUnroll; ++k) sum += sum_squares(v[k]);
   }
   const double t = cta_sum<kThreads>(sum);
   if (threadIdx.x == 0) partials[blockIdx.x] = t;

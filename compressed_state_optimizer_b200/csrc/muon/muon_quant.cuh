@@ -133,31 +133,39 @@ __device__ __forceinline__ void unpack8(uint2 w, uint64_t (&q)[4]) {
   }
 }
 
+// A lane's 8 codes at p.
+template <int BITS>
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p) {
+  if constexpr (BITS == 8)
+    return *reinterpret_cast<const uint2*>(p);
+  else
+    return make_uint2(*reinterpret_cast<const uint32_t*>(p), 0u);
+}
 template <int BITS>
 __device__ __forceinline__ uint2 load_codes(const uint8_t* codes, int64_t block, int sub) {
-  if constexpr (BITS == 8) {
-    return *reinterpret_cast<const uint2*>(codes + block * kMuonBlock + 8 * sub);
-  } else {
-    return make_uint2(
-        *reinterpret_cast<const uint32_t*>(codes + block * (kMuonBlock / 2) + 4 * sub), 0u);
-  }
+  return load_codes<BITS>(codes + (block * kMuonBlock + 8 * sub) * BITS / 8);
 }
-
 template <int BITS>
-__device__ __forceinline__ void store_codes(uint8_t* codes, int64_t block, int sub,
-                                            const uint32_t (&c)[8]) {
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&c)[8]) {
   if constexpr (BITS == 8) {
     const uint32_t a = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040),
                                    0x5410);
     const uint32_t b = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040),
                                    0x5410);
-    *reinterpret_cast<uint2*>(codes + block * kMuonBlock + 8 * sub) = make_uint2(a, b);
+    *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
   } else {
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w |= (c[e] & 15u) << (4 * e);
-    *reinterpret_cast<uint32_t*>(codes + block * (kMuonBlock / 2) + 4 * sub) = w;
+    // Bytes of the even and of the odd values, merged nibble by nibble.
+    const uint32_t even = __byte_perm(__byte_perm(c[0], c[2], 0x0040),
+                                      __byte_perm(c[4], c[6], 0x0040), 0x5410);
+    const uint32_t odd = __byte_perm(__byte_perm(c[1], c[3], 0x0040),
+                                     __byte_perm(c[5], c[7], 0x0040), 0x5410);
+    *reinterpret_cast<uint32_t*>(p) = (even & 0x0F0F0F0Fu) | ((odd << 4) & 0xF0F0F0F0u);
   }
+}
+template <int BITS>
+__device__ __forceinline__ void store_codes(uint8_t* codes, int64_t block, int sub,
+                                            const uint32_t (&c)[8]) {
+  store_codes<BITS>(codes + (block * kMuonBlock + 8 * sub) * BITS / 8, c);
 }
 
 // Scale and its reciprocal of a block whose largest magnitude is a. A block
@@ -173,16 +181,31 @@ __device__ __forceinline__ void block_scale(float a, float level_recip, float& s
   }
 }
 
-// The larger magnitude, NaN if either is.
+// The larger magnitude, NaN if either is; the sign means nothing.
 __device__ __forceinline__ float max_magnitude(float a, float b) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 __device__ __forceinline__ float half_warp_max(float v) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) v = max_magnitude(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
+  return fabsf(v);
+}
+
+// philox4x32_10 of mua_kernels.cuh with each round's two products as one wide
+// multiplication each.
+__device__ __forceinline__ uint4 philox_wide(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3,
+                                             const uint32_t (&keys)[10][2]) {
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
+    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ keys[r][0];
+    c1 = (uint32_t)p1;
+    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ keys[r][1];
+    c3 = (uint32_t)p0;
+  }
+  return make_uint4(c0, c1, c2, c3);
 }
 
 template <int BITS>
@@ -225,9 +248,9 @@ __device__ __forceinline__ void quantize_block(uint64_t (&m)[4], int left, uint6
   top = half_warp_max(top);
   float inverse;
   block_scale(top, Level<BITS>::recip, scale, inverse);
-  bad = bad || !(top < __uint_as_float(0x7F800000u));
+  bad |= !(top < __uint_as_float(0x7F800000u));
   const uint4 w =
-      philox4x32_10((uint32_t)counter, (uint32_t)(counter >> 32), rnd.t_lo, rnd.t_hi, rnd.keys);
+      philox_wide((uint32_t)counter, (uint32_t)(counter >> 32), rnd.t_lo, rnd.t_hi, rnd.keys);
   const uint64_t inv2 = f2_splat(inverse), step = f2_splat(1.52587890625e-05f);
   const uint64_t magic = f2_splat(12582784.0f);  // 1.5 2^23 - 128
 #pragma unroll
@@ -268,7 +291,8 @@ __device__ __forceinline__ double sum_squares(const uint64_t (&v)[4]) {
 #pragma unroll
   for (int e = 1; e < 4; ++e) t = f2_fma_rn(v[e], v[e], t);
   const float f = f2_lo(t) + f2_hi(t);
-  if (f > 1e-20f && f < 1e30f) return (double)f;
+  if ((f > 1e-20f && f < 1e30f) || (t == 0 && v[0] == 0 && v[1] == 0 && v[2] == 0 && v[3] == 0))
+    return (double)f;
   double s = 0.0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
