@@ -191,32 +191,40 @@ int iterate(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count, co
 }
 
 // Time of a step's products on tiles of bn, in us: per product the waves of
-// items over the SMs, an item's k-slices or (where longer) its epilogue, and the
-// way from one product's last store to the next one's first MMA. Measured: a
-// 64-deep slice 0.33 us on 256 x 256 tiles of CTA pairs, 0.21 us on 128 x 128;
-// an epilogue 1.5 and 0.9 us; between products 3.5 us. The larger tile wins
-// from about 2048 x 2048 or 8 x 1024 x 1024 on, the smaller one below
-// (512 x 512: 103 against 126 us, 16 x 300 x 300: 100 against 147 us).
+// items over the SMs (whole ones for a single matrix; those of a stack overlap),
+// an item's k-slices and what it adds to them, and the way from one product's
+// last store to the next one's first MMA. Fitted to measurements: a 64-deep
+// slice takes 0.30 us on 256 x 256 tiles of CTA pairs and 0.28 us on 128 x 128
+// (32 KB an SM either way, the rate of L2), an item 2 and 0.7 us more, between
+// products 4.2 us. So the larger tile, with four times the work a slice, wins
+// from about 2048 x 2048 (245 against 249 us) or 8 x 1024 x 1024 (208, 224 us)
+// on, the smaller one where its items fit the SMs at once: 768 x 768 (108, 140),
+// 5 x 1000 x 333 (104, 139). Sharing A's tiles among idle SMs costs a product
+// more: 512 x 11008 343 -> 184 us, but 5 x 1000 x 333 104 -> 123 us.
 Tiling tiling(int32_t rows, int32_t cols, int32_t batch, int32_t bn) {
   const bool big = bn == 256;
-  const double slice = big ? 0.33 : 0.21, epilogue = big ? 1.5 : 0.9, between = 3.5;
+  const double slice = big ? 0.30 : 0.28, item = big ? 2.0 : 0.7, between = 4.2;
   const int64_t units = big ? 74 : 148;  // CTA pairs or CTAs of a B200
   const int64_t s = std::min(rows, cols), l = std::max(rows, cols);
   const int64_t tm = (s + bn - 1) / bn, sym = tm * (tm + 1) / 2 * batch;
   const int64_t upd = (int64_t)((rows + bn - 1) / bn) * ((cols + bn - 1) / bn) * batch;
   const int64_t gram = (l + 63) / 64, update = (s + 63) / 64;
-  Tiling t = {bn, 1, 1, 0.0};
-  // A's tiles split over idle SMs while a share keeps 8 slices.
+  auto product = [&](int64_t items, double slices) {
+    const double waves = std::max(1.0, (double)items / units);
+    return (batch > 1 ? waves : std::ceil(waves)) * (slices * slice + item) + between;
+  };
+  Tiling t = {bn, 1, 1, product(sym, gram)};
+  // A share keeps 8 slices or more.
   const int64_t split = std::min<int64_t>(std::min<int64_t>(16, units / sym), gram / 8);
   if (split > 1) {
-    t.split = (int32_t)split;
-    while (2 * t.reduce <= t.split) t.reduce *= 2;
+    const double us = product(sym * split, (double)gram / split) + item + between;
+    if (us < t.us) {
+      t.us = us;
+      t.split = (int32_t)split;
+      while (2 * t.reduce <= t.split) t.reduce *= 2;
+    }
   }
-  auto product = [&](int64_t items, int64_t slices) {
-    return (double)((items + units - 1) / units) * std::max(slices * slice, epilogue) + between;
-  };
-  t.us = product(sym * t.split, gram / t.split) + product(sym, update) + product(upd, update);
-  if (t.split > 1) t.us += epilogue + between;
+  t.us += product(sym, update) + product(upd, update);
   return t;
 }
 

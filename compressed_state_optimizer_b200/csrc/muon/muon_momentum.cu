@@ -125,7 +125,7 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
 
 // Partial sums of U^2: as momentum_kernel, without a write to the state.
 template <int BITS, int G>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 direction_norm_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nesterov,
                       double* partials) {
   wait_previous();
@@ -175,7 +175,7 @@ direction_norm_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int n
 // Groups of 8 values of one row of a strided stack; a contiguous matrix counts
 // as one row of rows * cols values.
 template <int T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 norm_kernel(MuonShape s, MuonView x, double* partials) {
   wait_previous();
   release_next();
