@@ -4,11 +4,15 @@
 // global memory is read once or twice at the start and written once at the end.
 //
 // Each of the 3 products per step is a handful of MMAs, issued by a warp of
-// their own, followed by an epilogue of the 16 others, so a step is bound by the latency of issue, completion,
-// TMEM read and CTA barrier, not by arithmetic. X has the caller's orientation
-// (s = short, l = long side): a wide one is s rows of ceil(l / 64) chunks, a
-// tall one l rows of ceil(s / 64) chunks, rows and contracted columns padded
-// with zeros to 16. An MMA always covers 128 rows; those behind the last are
+// their own, followed by an epilogue of the 16 others, so a step is bound by the
+// latency of issue, completion, TMEM read and the hand-over, not by arithmetic.
+// The issuing warp runs a loop of its own: where it shared one with the others
+// it waited some 300 cycles for instructions at every product.
+//
+// X lies with its long side along the rows of shared memory whichever way the
+// caller has it (s = short, l = long side): s rows of ceil(l / 64) chunks,
+// padded with zeros to 16 rows and columns; a tall matrix is transposed as it is
+// read and written. An MMA always covers 128 rows; those behind the last are
 // whatever shared memory holds there, and only make accumulator rows that
 // nothing reads.
 #include "muon_quant.cuh"
@@ -26,9 +30,9 @@ __host__ __device__ __forceinline__ int round16(int x) { return (x + 15) & ~15; 
 
 struct Plan {
   int s, l, s16, l16;     // short and long side, padded
-  bool tall;
+  bool tall;              // rows > cols
   int ns, chunks;         // 64-wide chunks of the short side; of X
-  uint32_t xs, ps;        // bytes of a chunk of X, of A and P
+  uint32_t xs;            // bytes of a chunk of X, A and P: s16 rows of 128
   uint32_t a_off, p_off, bytes;
   uint32_t columns;       // of TMEM
 };
@@ -40,12 +44,11 @@ __host__ __device__ __forceinline__ Plan plan_of(int rows, int cols) {
   p.s16 = round16(p.s);
   p.l16 = round16(p.l);
   p.ns = (p.s + 63) / 64;
-  p.chunks = p.tall ? p.ns : (p.l + 63) / 64;
-  p.xs = (uint32_t)(p.tall ? p.l16 : p.s16) * 128u;
-  p.ps = (uint32_t)p.s16 * 128u;
+  p.chunks = (p.l + 63) / 64;
+  p.xs = (uint32_t)p.s16 * 128u;
   p.a_off = (uint32_t)p.chunks * p.xs;
-  p.p_off = p.a_off + (uint32_t)p.ns * p.ps;
-  p.bytes = p.p_off + (uint32_t)p.ns * p.ps + kOverread;
+  p.p_off = p.a_off + (uint32_t)p.ns * p.xs;
+  p.bytes = p.p_off + (uint32_t)p.ns * p.xs + kOverread;
   const int update = (p.l + 127) / 128 * p.s16;
   const int need = update > 512 ? 512 : (update > p.s16 ? update : p.s16);
   p.columns = 32;
@@ -57,6 +60,14 @@ __host__ __device__ __forceinline__ Plan plan_of(int rows, int cols) {
 __device__ __forceinline__ uint32_t group_address(uint32_t tile, uint32_t chunk_bytes, int row,
                                                   int col) {
   return chunk_address(tile + (uint32_t)(col >> 6) * chunk_bytes, row, (col >> 3) & 7);
+}
+
+// Value (j, i) of X, j along the short side.
+__device__ __forceinline__ uint32_t value_address(uint32_t X, uint32_t xs, int j, int i) {
+  return group_address(X, xs, j, i) + 2u * (i & 7);
+}
+__device__ __forceinline__ void st_half(uint32_t at, uint32_t bits) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)bits) : "memory");
 }
 
 // The last product's 16 values of a lane, `left` of them inside the matrix, in
@@ -116,7 +127,8 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
   constexpr int T = SRC & 1;                       // value type of x or the gradients
   constexpr int BITS = SRC >= 4 ? 4 : 8;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t done;
+  // MMAs of a product complete; taken over by every worker warp; all complete.
+  __shared__ __align__(8) uint64_t done, ready, drained;
   __shared__ uint32_t tmem_base_s, stop;
   __shared__ NormScale scale_s;
   const Plan p = plan_of(sh.rows, sh.cols);
@@ -128,6 +140,8 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&done), 1);
+    mbar_init(smem_u32(&ready), kWorkers / 32);
+    mbar_init(smem_u32(&drained), 1);
     stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -149,7 +163,15 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     const int es = T == kBf16 ? 2 : 4;
     const uint8_t* xm = static_cast<const uint8_t*>(x.p) + mat * x.matrix_stride * es;
     const bool vec = aligned16(xm) && (x.row_stride * es) % 16 == 0;
+    // Groups of 8 columns: along a row for a wide matrix, down the rows for a tall
+    // one, whose neighbouring lanes then write neighbouring columns of X.
     const uint32_t per_row = (uint32_t)(sh.cols + 7) / 8, groups = per_row * (uint32_t)sh.rows;
+    const uint32_t line = p.tall ? (uint32_t)sh.rows : per_row;
+    auto place = [&](uint32_t q, int& row, int& col) {
+      const uint32_t a = q / line, b = q - a * line;
+      row = (int)(p.tall ? b : a);
+      col = 8 * (int)(p.tall ? a : b);
+    };
     double sum = 0.0;
     // Up to kHeld groups of 8 per thread stay in registers between the passes.
     constexpr int kHeld = 2;
@@ -158,9 +180,9 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
         const uint32_t q = q0 + k * kWorkers;
-        const uint32_t row = q / per_row, col = 8 * (q - row * per_row);
-        const int64_t end = q < groups ? sh.cols : 0;
-        load8<T>(xm + (int64_t)row * x.row_stride * es, col, end, vec, held[k]);
+        int row, col;
+        place(q, row, col);
+        load8<T>(xm + (int64_t)row * x.row_stride * es, col, q < groups ? sh.cols : 0, vec, held[k]);
       }
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) sum += sum_squares(held[k]);
@@ -171,7 +193,8 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     const NormScale ns = scale_s;
 #pragma unroll 1
     for (uint32_t q = threadIdx.x, k = 0; worker && q < groups; q += kWorkers, ++k) {
-      const uint32_t row = q / per_row, col = 8 * (q - row * per_row);
+      int row, col;
+      place(q, row, col);
       uint64_t v[4];
       if (groups > kHeld * kWorkers) {
         load8<T>(xm + (int64_t)row * x.row_stride * es, col, sh.cols, vec, v);
@@ -180,7 +203,15 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
         for (int e = 0; e < 4; ++e) v[e] = k == 0 ? held[0][e] : held[1][e];
       }
       const uint4 h = scaled_f16(v, ns.first, ns.second);
-      st_shared(group_address(X, p.xs, (int)row, (int)col), h.x, h.y, h.z, h.w);
+      if (!p.tall) {
+        st_shared(group_address(X, p.xs, row, col), h.x, h.y, h.z, h.w);
+      } else {
+        const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col + e < sh.cols)
+            st_half(value_address(X, p.xs, col + e, row), hw[e >> 1] >> (16 * (e & 1)));
+      }
     }
   } else {
     const int half = threadIdx.x >> 4, sub = threadIdx.x & 15;
@@ -253,17 +284,15 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
           int row = (int)((uint32_t)i / (uint32_t)sh.cols);
           int col = (int)i - row * sh.cols;
           const uint4 h = scaled_f16(u, ns.first, ns.second);
-          if ((sh.cols & 7) == 0) {  // eight values of one row
+          if (!p.tall && (sh.cols & 7) == 0) {  // eight values of one row
             if (left > 0) st_shared(group_address(X, p.xs, row, col), h.x, h.y, h.z, h.w);
           } else {
             const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               if (e < left)
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(group_address(X, p.xs, row, col) +
-                                                             2u * (col & 7)),
-                             "h"((uint16_t)(hw[e >> 1] >> (16 * (e & 1))))
-                             : "memory");
+                st_half(value_address(X, p.xs, p.tall ? col : row, p.tall ? row : col),
+                        hw[e >> 1] >> (16 * (e & 1)));
               if (++col == sh.cols) {
                 col = 0;
                 ++row;
@@ -281,207 +310,199 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
   fence_after();
 
   const uint32_t tmem = tmem_base_s;
-  const float factor = scale_s.factor;
-  const int quarter = warp & 3, part = warp >> 2;     // TMEM lanes; every fourth 16 columns
-  const int lane_row = quarter * 32 + lane;
-  const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-  const int sunits = p.s16 / 16;
   volatile uint32_t* stop_v = &stop;
-  uint32_t turn = 0;
+  const int sunits = p.s16 / 16;
+  const int tiles = (p.l + 127) / 128, pass = 512 / p.s16;  // of X', in TMEM at once
+  uint32_t stage = 0;  // products begun, counting the update's passes
   bool ok = true;
-  // Waits for the MMAs issued. A thread that gives up goes on to the next
-  // publish(), where the CTA stops as one; what it reads until then is unused.
-  auto finish = [&]() {
-    ok = mbar_wait(smem_u32(&done), turn, g.wait_ns, stop_v);
-    fence_after();
-  };
-  // Every thread's tile writes and TMEM reads come before the next MMAs.
-  auto publish = [&]() {
-    fence_async_shared();
-    fence_before();
-    ok = __syncthreads_or(!ok) == 0;
-    fence_after();
-    if (ok) turn ^= 1u;
-    return ok;
-  };
 
-  // The issuing warp runs converged (descriptors stay in uniform registers).
-  const uint32_t sym_idesc = instruction_desc<1>(p.s16, false, false);
-  for (int k = 0; ok && k < g.steps; ++k) {
-    // A = f^2 X X^T
-    if (!worker) {
-      const bool lead = elect_one();
-      if (p.tall) {
-        const uint32_t idesc = instruction_desc<1>(p.s16, true, true);
-        // 64 further rows of A behind a single chunk: the chunk again.
-        uint64_t d = operand_desc(X, p.ns > 1 ? p.xs : 0);
-        for (int kk = 0; kk < p.l16 / 16; ++kk, d += 2048 >> 4)
-          if (lead) mma_f16<1>(tmem, d, d, idesc, kk != 0);
-      } else {
-        uint64_t chunk = operand_desc(X, 16);
-        for (int left = p.l16 / 16, first = 1; left > 0; left -= 4, chunk += p.xs >> 4) {
-          uint64_t d = chunk;
-          for (int kk = 0; kk < min(4, left); ++kk, d += 32 >> 4, first = 0)
-            if (lead) mma_f16<1>(tmem, d, d, sym_idesc, first == 0);
-        }
+  if (!worker) {
+    const bool lead = elect_one();
+    const uint32_t sym = instruction_desc<1>(p.s16, false, false);
+    const uint32_t upd = instruction_desc<1>(p.s16, true, false);
+    const uint64_t x0 = operand_desc(X, 16), a0 = operand_desc(A, 16), p0 = operand_desc(P, 16);
+    const uint64_t xt = operand_desc(X, p.xs);  // X by its columns
+    const uint32_t chunk = p.xs >> 4;
+    // `depth` k-steps of 16 along the rows of two operands.
+    auto along = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int depth) {
+      for (int kk = 0; kk < depth; ++kk) {
+        if (lead) mma_f16<1>(d, a, b, idesc, kk != 0);
+        const uint32_t step = (kk & 3) == 3 ? chunk - 6 : 2;
+        a += step;
+        b += step;
       }
+    };
+    // The others have taken the last product over.
+    auto begin = [&]() {
+      if (stage > 0) ok = mbar_wait_warp(smem_u32(&ready), (stage - 1) & 1u, g.wait_ns, stop_v);
+      fence_after();
+      ++stage;
+      return ok;
+    };
+    for (int k = 0; ok && k < g.steps; ++k) {
+      if (!begin()) break;
+      along(tmem, x0, x0, sym, p.l16 / 16);  // X X^T
       if (lead) mma_commit<1>(smem_u32(&done));
-      __syncwarp();
-    }
-    finish();
-    uint32_t held[2][8];  // this thread's part of A, for the next product
-    if (worker && quarter * 32 < p.s16) {
-      const float alpha = k == 0 ? g.gram_alpha[0] * factor * factor : g.gram_alpha[k];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int u = part + 4 * q;
-        if (u < sunits) {
-          uint32_t v[16];
-          tmem_load16(lanes + 16 * u, v);
-          tmem_load_wait();
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            held[q][e] = pack_f16(__uint_as_float(v[2 * e]) * alpha,
-                                  __uint_as_float(v[2 * e + 1]) * alpha);
-          if (lane_row < p.s16) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              st_shared(group_address(A, p.ps, lane_row, 16 * u + 8 * h), held[q][4 * h],
-                        held[q][4 * h + 1], held[q][4 * h + 2], held[q][4 * h + 3]);
-          }
-          __syncwarp();
-        }
-      }
-    }
-    if (!publish()) break;
-
-    // P = a I + b A + c A A
-    if (!worker) {
-      const bool lead = elect_one();
-      uint64_t chunk = operand_desc(A, 16);
-      for (int left = sunits, first = 1; left > 0; left -= 4, chunk += p.ps >> 4) {
-        uint64_t d = chunk;
-        for (int kk = 0; kk < min(4, left); ++kk, d += 32 >> 4, first = 0)
-          if (lead) mma_f16<1>(tmem, d, d, sym_idesc, first == 0);
-      }
+      if (!begin()) break;
+      along(tmem, a0, a0, sym, sunits);      // A A
       if (lead) mma_commit<1>(smem_u32(&done));
-      __syncwarp();
-    }
-    finish();
-    if (worker && quarter * 32 < p.s16) {
-      const float alpha = g.poly_alpha[k], mid = g.poly_mid[k], diag = g.poly_diag[k];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int u = part + 4 * q;
-        if (u < sunits) {
-          uint32_t v[16];
-          tmem_load16(lanes + 16 * u, v);
-          tmem_load_wait();
-          const int diagonal = lane_row < p.s ? lane_row - 16 * u : -1;
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&held[q][e]));
-            float x0 = fmaf(y.x, mid, __uint_as_float(v[2 * e]) * alpha);
-            float x1 = fmaf(y.y, mid, __uint_as_float(v[2 * e + 1]) * alpha);
-            if (2 * e == diagonal) x0 += diag;
-            if (2 * e + 1 == diagonal) x1 += diag;
-            w[e] = pack_f16(x0, x1);
-          }
-          if (lane_row < p.s16) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              st_shared(group_address(P, p.ps, lane_row, 16 * u + 8 * h), w[4 * h], w[4 * h + 1],
-                        w[4 * h + 2], w[4 * h + 3]);
-          }
-          __syncwarp();
-        }
-      }
-    }
-    if (!publish()) break;
-
-    // X' = f P X (X P), with the long side along the accumulator rows either
-    // way so that all TMEM lanes work: tile t holds its rows 128 t .. in columns
-    // s16 t .. of a pass of up to 512 columns. A pass replaces only what no
-    // other tile reads.
-    const bool last = k == g.steps - 1;
-    const float alpha = k == 0 ? g.update_alpha[0] * factor : g.update_alpha[k];
-    const int tiles = (p.l + 127) / 128, pass = 512 / p.s16;
-    for (int p0 = 0; ok && p0 < tiles; p0 += pass) {
-      const int now = min(pass, tiles - p0);
-      if (!worker) {
-        const bool lead = elect_one();
-        const uint32_t idesc = instruction_desc<1>(p.s16, !p.tall, false);
-        // Tall: rows of X, 16 columns a step, 64 a chunk. Wide: columns of X (two
-        // chunks a tile), 16 rows a step.
-        uint64_t tile = p.tall ? operand_desc(X + p0 * 16384, 16)
-                               : operand_desc(X + 2 * p0 * p.xs, p.xs);
-        const uint64_t tile_step = p.tall ? 16384 >> 4 : (2 * p.xs) >> 4;
-        const uint64_t a_step = p.tall ? 32 >> 4 : 2048 >> 4;
-        const uint64_t a_chunk = p.tall ? p.xs >> 4 : 4 * (2048 >> 4);
-        const uint64_t b0 = operand_desc(P, 16);
-        for (int t = 0; t < now; ++t, tile += tile_step) {
-          uint64_t a_at = tile, b_at = b0;
-          for (int left = sunits, first = 1; left > 0;
-               left -= 4, a_at += a_chunk, b_at += p.ps >> 4) {
-            uint64_t a = a_at, b = b_at;
-            for (int kk = 0; kk < min(4, left); ++kk, a += a_step, b += 32 >> 4, first = 0)
-              if (lead) mma_f16<1>(tmem + t * p.s16, a, b, idesc, first == 0);
+      for (int t0 = 0; t0 < tiles; t0 += pass) {
+        if (!begin()) break;
+        // X^T P: 128 columns of X (two chunks) a tile, 16 rows a step.
+        uint64_t a_tile = xt + (uint32_t)t0 * 2 * chunk;
+        const int now = min(pass, tiles - t0);
+        for (int t = 0; t < now; ++t, a_tile += 2 * chunk) {
+          uint64_t a = a_tile, b = p0;
+          for (int kk = 0; kk < sunits; ++kk) {
+            if (lead) mma_f16<1>(tmem + t * p.s16, a, b, upd, kk != 0);
+            a += 2048 >> 4;
+            b += (kk & 3) == 3 ? chunk - 6 : 2;
           }
         }
         if (lead) mma_commit<1>(smem_u32(&done));
-        __syncwarp();
       }
-      finish();
-      for (int u = part; worker && u < now * sunits; u += 4) {
-        const int t = u / sunits, j0 = 16 * (u - t * sunits);  // short side j0 .. j0 + 15
-        const int i0 = (p0 + t) * 128 + quarter * 32;          // long side
-        if (i0 >= p.l16) continue;
-        const int i = i0 + lane;
-        if (last) {
-          const int64_t at = mat * g.batch_stride + (p.tall ? i * g.ldo + j0 : j0 * g.ldo + i);
-          if (p.tall)
-            finish_columns(g, lanes + 16 * u, at, i < p.l ? p.s - j0 : 0, alpha);
-          else
-            finish_rows(g, lanes + 16 * u, at, i < p.l ? p.s - j0 : 0, alpha);
-          continue;
-        }
-        uint32_t v[16], w[8];
-        tmem_load16(lanes + 16 * u, v);
-        tmem_load_wait();
+    }
+    __syncwarp();
+  } else {
+    const float factor = scale_s.factor;
+    const int quarter = warp & 3, part = warp >> 2;  // TMEM lanes; every fourth 16 columns
+    const int lane_row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    // The next product's MMAs are complete.
+    auto take = [&]() {
+      ok = mbar_wait_warp(smem_u32(&done), stage & 1u, g.wait_ns, stop_v);
+      fence_after();
+      ++stage;
+      return ok;
+    };
+    // This warp has read its part of them and written what the next one reads.
+    auto hand_over = [&]() {
+      fence_async_shared();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ready));
+    };
+    for (int k = 0; k < g.steps; ++k) {
+      // A = f^2 X X^T
+      if (!take()) break;
+      uint32_t held[2][8];  // this thread's part of A, for the next product
+      if (quarter * 32 < p.s16) {
+        const float alpha = k == 0 ? g.gram_alpha[0] * factor * factor : g.gram_alpha[k];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          w[e] = pack_f16(__uint_as_float(v[2 * e]) * alpha, __uint_as_float(v[2 * e + 1]) * alpha);
-        if (p.tall) {
-          if (i < p.l16) {
+        for (int q = 0; q < 2; ++q) {
+          const int u = part + 4 * q;
+          if (u < sunits) {
+            uint32_t v[16];
+            tmem_load16(lanes + 16 * u, v);
+            tmem_load_wait();
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              st_shared(group_address(X, p.xs, i, j0 + 8 * h), w[4 * h], w[4 * h + 1],
-                        w[4 * h + 2], w[4 * h + 3]);
+            for (int e = 0; e < 8; ++e)
+              held[q][e] = pack_f16(__uint_as_float(v[2 * e]) * alpha,
+                                    __uint_as_float(v[2 * e + 1]) * alpha);
+            if (lane_row < p.s16) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                st_shared(group_address(A, p.xs, lane_row, 16 * u + 8 * h), held[q][4 * h],
+                          held[q][4 * h + 1], held[q][4 * h + 2], held[q][4 * h + 3]);
+            }
+            __syncwarp();
           }
-        } else if (i < p.l16) {
-          // A lane's value of 16 rows: 32 lanes write 64 contiguous bytes of each.
-          // Rows j0 + e, with j0 a multiple of 16, swizzle by e & 7.
-          const uint32_t base = X + (uint32_t)(i >> 6) * p.xs + j0 * 128 + 2 * (i & 7);
-          const uint32_t group = (uint32_t)(i & 56) << 1;
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(base + e * 128 +
-                                                         (group ^ ((e & 7) << 4))),
-                         "h"((uint16_t)(w[e >> 1] >> (16 * (e & 1))))
-                         : "memory");
         }
-        __syncwarp();
       }
-      if (!publish()) break;
+      hand_over();
+
+      // P = a I + b A + c A A
+      if (!take()) break;
+      if (quarter * 32 < p.s16) {
+        const float alpha = g.poly_alpha[k], mid = g.poly_mid[k], diag = g.poly_diag[k];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int u = part + 4 * q;
+          if (u < sunits) {
+            uint32_t v[16];
+            tmem_load16(lanes + 16 * u, v);
+            tmem_load_wait();
+            const int diagonal = lane_row < p.s ? lane_row - 16 * u : -1;
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&held[q][e]));
+              float x0 = fmaf(y.x, mid, __uint_as_float(v[2 * e]) * alpha);
+              float x1 = fmaf(y.y, mid, __uint_as_float(v[2 * e + 1]) * alpha);
+              if (2 * e == diagonal) x0 += diag;
+              if (2 * e + 1 == diagonal) x1 += diag;
+              w[e] = pack_f16(x0, x1);
+            }
+            if (lane_row < p.s16) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                st_shared(group_address(P, p.xs, lane_row, 16 * u + 8 * h), w[4 * h], w[4 * h + 1],
+                          w[4 * h + 2], w[4 * h + 3]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      hand_over();
+
+      // X' = f P X, with the long side along the accumulator rows so that all TMEM
+      // lanes work: tile t holds its rows 128 t .. in columns s16 t .. of a pass of
+      // up to 512 columns. A pass replaces only what no other tile reads.
+      const bool last = k == g.steps - 1;
+      const float alpha = k == 0 ? g.update_alpha[0] * factor : g.update_alpha[k];
+      for (int t0 = 0; t0 < tiles; t0 += pass) {
+        const int now = min(pass, tiles - t0);
+        if (!take()) break;
+        for (int u = part; u < now * sunits; u += 4) {
+          const int t = u / sunits, j0 = 16 * (u - t * sunits);  // short side j0 .. j0 + 15
+          const int i0 = (t0 + t) * 128 + quarter * 32;          // long side
+          if (i0 >= p.l16) continue;
+          const int i = i0 + lane;
+          if (last) {
+            const int64_t at = mat * g.batch_stride + (p.tall ? i * g.ldo + j0 : j0 * g.ldo + i);
+            if (p.tall)
+              finish_columns(g, lanes + 16 * u, at, i < p.l ? p.s - j0 : 0, alpha);
+            else
+              finish_rows(g, lanes + 16 * u, at, i < p.l ? p.s - j0 : 0, alpha);
+            continue;
+          }
+          uint32_t v[16];
+          tmem_load16(lanes + 16 * u, v);
+          tmem_load_wait();
+          if (i < p.l16) {
+            // A lane's value of 16 rows: 32 lanes write 64 contiguous bytes of each.
+            // Rows j0 + e, with j0 a multiple of 16, swizzle by e & 7.
+            const uint32_t base = X + (uint32_t)(i >> 6) * p.xs + j0 * 128 + 2 * (i & 7);
+            const uint32_t group = (uint32_t)(i & 56) << 1;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t w = pack_f16(__uint_as_float(v[2 * e]) * alpha,
+                                          __uint_as_float(v[2 * e + 1]) * alpha);
+              st_half(base + (2 * e) * 128 + (group ^ ((2 * e & 7) << 4)), w);
+              st_half(base + (2 * e + 1) * 128 + (group ^ ((2 * e + 1 & 7) << 4)), w >> 16);
+            }
+          }
+          __syncwarp();
+        }
+        hand_over();
+      }
+      if (!ok) break;
     }
   }
-  // MMAs in flight end before shared memory and TMEM go.
-  if (!ok) mbar_drain(smem_u32(&done), turn);
+  __syncwarp();
+  fence_before();
   __syncthreads();
-  if (!worker)
+  fence_after();
+  // MMAs in flight end before shared memory and TMEM go.
+  if (!worker) {
+    if (stop_v[0] != 0 && stage > 0) {
+      if (elect_one()) mma_commit<1>(smem_u32(&drained));
+      mbar_drain(smem_u32(&drained), 0);
+    }
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(p.columns));
+  }
   if (threadIdx.x == 0 && stop) atomicOr(g.status, kMuonTimeout);
 }
 
