@@ -18,10 +18,10 @@
 // 12) or 128 x 128 on one CTA when the 256-wide tiles would be too few for the
 // SMs. Per CTA: warps 0 and 10 stream 64-deep slices of the operands A and B
 // into a ring of 128-byte swizzled shared tiles (TMA), warp 1 issues the MMAs,
-// warps 2..9 turn finished accumulators into a tile in shared memory while the
-// next tile's MMAs run into the other half of TMEM, and warp 11 moves that tile
-// out (the addend of P in before), waits for it to be in memory and counts it,
-// so that nothing else stands still for it. The instructions between two slices' MMAs are
+// warps 2..9 write finished accumulators out, through shared memory into whole
+// lines, while the next tile's MMAs run into the other half of TMEM, and warp 11
+// brings the addend of P in and counts finished tiles, so that nothing else
+// stands still for those. The instructions between two slices' MMAs are
 // what bounds the rate next to the tensor cores (256 cycles of MMA a slice on
 // 128 x 128, 512 on 256 x 256): hence a warp for each operand, one copy for an
 // operand whose rows are contiguous in depth, and majors fixed per item.
@@ -51,7 +51,7 @@ struct Ring {
 };
 struct Maps {
   // X of even and odd steps, A, P: boxes of 64 columns by 128 rows (an operand's
-  // rows, and the output) and by 64 rows (an operand's columns).
+  // rows) and by 64 rows (an operand's columns).
   CUtensorMap rows[4], cols[4];
 };
 
@@ -200,17 +200,18 @@ __device__ __forceinline__ int first_mn(const MuonNs& g, const Item& it, bool a)
   return tall ? never : 0;
 }
 
+__device__ __forceinline__ bool matrix_ready(const MuonNs& g, int z, uint32_t want) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(g.counters + z) : "memory");
+  return v >= want;
+}
 // Waits until matrix z has `want` finished items (every CTA of an item counts
 // one). Items are taken in order by CTAs that are all resident, and
 // need earlier items only, so the wait ends.
 __device__ __forceinline__ bool matrix_wait(const MuonNs& g, int z, uint32_t want,
                                             volatile uint32_t* stop) {
-  const uint32_t* p = g.counters + z;
   uint64_t t0 = 0;
-  for (uint32_t n = 1;; ++n) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    if (v >= want) return true;
+  for (uint32_t n = 1; !matrix_ready(g, z, want); ++n) {
     if (g.wait_ns != 0 && (n & 63u) != 0) continue;
     if (*stop) return false;
     const uint64_t t = now_ns();
@@ -220,6 +221,7 @@ __device__ __forceinline__ bool matrix_wait(const MuonNs& g, int z, uint32_t wan
       return false;
     }
   }
+  return true;
 }
 
 // This CTA's part of an item is in memory: count it.
@@ -289,7 +291,8 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
   constexpr uint32_t kTmemCols = 2 * BN;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drained;
-  // The output tile in shared memory: all parts written; free again; P's addend there.
+  // An item's output: all warps have written theirs; the next one's may follow;
+  // P's addend is in shared memory.
   __shared__ __align__(8) uint64_t staged, room, addend;
   __shared__ uint32_t tmem_base_s, stop;
   __shared__ uint32_t issued_s[4];  // copies of A and of B, of this CTA and the pair's other
@@ -456,50 +459,42 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
     const bool elected = elect_one();
     uint32_t done = 0, addends = 0;  // items, and those with an addend
     bool ok = true;
-    for (Walk<BN> walk(g, first, stride); ok && walk.more(); walk.advance()) {
-      const Item it = walk.item();
-      if (it.last) break;
-      const int M = it.kind == kUpdate ? g.rows : min(g.rows, g.cols);
-      const int N = it.kind == kUpdate ? g.cols : M;
-      const int row0 = it.i * BN + (int)rank * 128;
-      // 64-column chunks of the tile that hold output, from its first column on.
-      const int chunks = row0 < M ? min(BN / 64, (N - it.j * BN + 63) / 64) : 0;
+    // The addend of a P tile: the chunks of 64 columns that hold output.
+    auto ask = [&](const Item& it) {
+      const int N = min(g.rows, g.cols), row0 = it.i * BN + (int)rank * 128;
+      const int chunks = row0 < N ? min(BN / 64, (N - it.j * BN + 63) / 64) : 0;
+      if (elected) {
+        fence_async_global();
+        if (chunks > 0)
+          mbar_expect(smem_u32(&addend), (uint32_t)chunks * kChunkBytes);
+        else
+          mbar_arrive(smem_u32(&addend));
+        for (int c = 0; c < chunks; ++c)
+          tma_load<1>(tile_base + c * kChunkBytes, &maps.rows[2], smem_u32(&addend),
+                      it.j * BN + 64 * c, row0, it.z);
+      }
+      __syncwarp();
+      ++addends;
+    };
+    Walk<BN> walk(g, first, stride);
+    Item it = walk.item();
+    while (ok && walk.more() && !it.last) {
       if (it.kind == kPoly) {
         ok = matrix_wait(g, it.z, it.before * CG, stop_v);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        if (elected) {
-          fence_async_global();
-          if (chunks > 0)
-            mbar_expect(smem_u32(&addend), (uint32_t)chunks * kChunkBytes);
-          else
-            mbar_arrive(smem_u32(&addend));
-          for (int c = 0; c < chunks; ++c)
-            tma_load<1>(tile_base + c * kChunkBytes, &maps.rows[2], smem_u32(&addend),
-                        it.j * BN + 64 * c, row0, it.z);
-        }
-        __syncwarp();
-        ++addends;
+        ask(it);
       }
       ok = mbar_wait_warp(smem_u32(&staged), done & 1u, g.wait_ns, stop_v);
       if (!ok) break;
       if (elected) {
-        if (it.kind != kReduce && !(it.kind == kGram && g.split > 1)) {
-          const CUtensorMap* out =
-              &maps.rows[it.kind == kGram ? 2 : (it.kind == kPoly ? 3 : (it.step & 1) ^ 1)];
-          for (int c = 0; c < chunks; ++c)
-            tma_store(out, tile_base + c * kChunkBytes, it.j * BN + 64 * c, row0, it.z);
-          tma_store_commit();
-          tma_store_read_wait();
-          mbar_arrive(smem_u32(&room));
-          tma_store_wait_all();
-        } else {
-          mbar_arrive(smem_u32(&room));
-        }
+        mbar_arrive(smem_u32(&room));
         count_item(g, it.z);
       }
       __syncwarp();
       ++done;
+      walk.advance();
+      it = walk.item();
     }
     if (addends > 0) mbar_drain(smem_u32(&addend), (addends - 1) & 1u);
   } else {
@@ -544,8 +539,6 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
       ok = mbar_wait_warp(smem_u32(&acc_full[acc]), (n >> 1) & 1u, g.wait_ns, stop_v);
       if (!ok) break;
       fence_after();
-      ok = mbar_wait_warp(smem_u32(&room), (out_items & 1u) ^ 1u, g.wait_ns, stop_v);
-      if (!ok) break;
       if (it.kind == kPoly) {
         ok = mbar_wait_warp(smem_u32(&addend), addends & 1u, g.wait_ns, stop_v);
         if (!ok) break;
@@ -556,6 +549,11 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
       const bool partial = it.kind == kGram && g.split > 1;
       if (!it.last && !partial) {
         const float mid = g.poly_mid[it.step], diag = g.poly_diag[it.step];
+        // The warp's rows of the fp16 output; whole groups of 8 columns fit its stride.
+        const int ldo = it.kind == kUpdate ? g.ld : g.lds;
+        __half* out = static_cast<__half*>(
+            it.kind == kGram ? g.a : (it.kind == kPoly ? g.p : g.x[(it.step & 1) ^ 1]));
+        out += ((int64_t)it.z * M + row0) * ldo + col0;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
           const uint32_t tile = stage + c * kChunkBytes;
@@ -579,6 +577,16 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
                                 __uint_as_float(v[q >> 2][(8 * q + 2 * e + 1) & 31]) * alpha);
               st_shared(chunk_address(tile, lane, q), h[0], h[1], h[2], h[3]);
             }
+          }
+          __syncwarp();
+          // Eight lanes write a row's 128 contiguous bytes.
+          const int col = 64 * c + 8 * (lane & 7);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int r = 4 * q + (lane >> 3);
+            const uint4 u = ld_shared(chunk_address(tile, r, lane & 7));
+            if (row0 + r < M && col0 + col < N)
+              *reinterpret_cast<uint4*>(out + (int64_t)r * ldo + col) = u;
           }
         }
       } else if (partial) {
@@ -645,11 +653,15 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
           mbar_arrive_cluster(peer_address(smem_u32(&acc_empty[acc]), 0));
         else
           mbar_arrive(smem_u32(&acc_empty[acc]));
-        if (!it.last) mbar_arrive(smem_u32(&staged));
       }
-      __syncwarp();
       ++n;
-      if (!it.last) ++out_items;
+      if (it.last) continue;
+      // No warp arrives for an item before all have arrived for the last one.
+      ok = mbar_wait_warp(smem_u32(&room), (out_items & 1u) ^ 1u, g.wait_ns, stop_v);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(smem_u32(&staged));
+      __syncwarp();
+      ++out_items;
     }
   }
   __syncwarp();
@@ -712,7 +724,7 @@ struct Operand {
 };
 
 // Copies of 64 contiguous elements x `box_rows` rows of a batch of row-major
-// matrices; what lies outside a matrix reads as 0 and is not written.
+// matrices; what lies outside a matrix reads as 0.
 cudaError_t make_map(const Operand& o, int batch, int box_rows, CUtensorMap* map) {
   EncodeFn encode;
   const cudaError_t e = encode_fn(&encode);
