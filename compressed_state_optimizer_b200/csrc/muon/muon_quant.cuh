@@ -25,6 +25,17 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // Arithmetic on pairs of fp32 values (packed instructions, each half rounded
 // by itself as the scalar one is).
 __device__ __forceinline__ uint64_t f2_splat(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ uint64_t f2_fma_rn(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// A product that the addition after it may not absorb: a packed multiplication
+// and a packed addition, both .rn, come out with one rounding (measured), two
+// scalar multiplications and a packed addition with two.
+__device__ __forceinline__ uint64_t f2_mul_apart(float a, uint64_t b) {
+  return f2_pack(__fmul_rn(a, f2_lo(b)), __fmul_rn(a, f2_hi(b)));
+}
 __device__ __forceinline__ uint64_t f2_add_rm(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -218,15 +229,15 @@ struct Level {
 __device__ __forceinline__ void new_momentum(const uint64_t (&q)[4], float scale,
                                              const uint64_t (&g)[4], float beta, int nesterov,
                                              uint64_t (&m)[4], uint64_t (&u)[4]) {
-  const uint64_t s2 = f2_splat(scale), b2 = f2_splat(beta);
+  const uint64_t s2 = f2_splat(scale);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    m[e] = f2_add_rn(f2_mul_rn(b2, f2_mul_rn(q[e], s2)), g[e]);
+    m[e] = f2_add_rn(f2_mul_apart(beta, f2_mul_rn(q[e], s2)), g[e]);
     u[e] = m[e];
   }
   if (nesterov) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) u[e] = f2_add_rn(f2_mul_rn(b2, m[e]), g[e]);
+    for (int e = 0; e < 4; ++e) u[e] = f2_add_rn(f2_mul_apart(beta, m[e]), g[e]);
   }
 }
 
@@ -279,11 +290,6 @@ __device__ __forceinline__ int left_of(int64_t i, int64_t n) {
   return (int)(i + 8 <= n ? 8 : (i < n ? n - i : 0));
 }
 
-__device__ __forceinline__ uint64_t f2_fma_rn(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 // Sum of 8 squares: in fp32 (a relative error of 2^-22 at most) where that holds
 // it, else in fp64, whose range holds every square.
 __device__ __forceinline__ double sum_squares(const uint64_t (&v)[4]) {

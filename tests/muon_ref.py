@@ -104,3 +104,19 @@ def orthogonalize_bound(x, steps=5, coefficients=None, eps=1e-7, exact_input=Fal
             err += U16 * np.sqrt(np.sum(s_next ** 2))
         s = s_next
     return 1.25 * err + 1e-12
+
+
+def momentum_f32(q, scales, g, beta, nesterov, draw, level):
+    """One update in fp32, an operation at a time as the state's definition has
+    it: (direction, new scales, new codes) of (blocks, 128) arrays."""
+    f = np.float32
+    beta = f(beta)
+    m = beta * (q.astype(f) * scales[:, None]) + g
+    u = beta * m + g if nesterov else m
+    top = np.abs(m).max(1)
+    s = np.where(top < f(2.0 ** -100), f(0), top * f(1.0 / level)).astype(f)
+    with np.errstate(divide="ignore"):
+        inv = np.where(s == 0, f(0), f(1) / s).astype(f)
+    y = np.clip(m * inv[:, None], f(-level), f(level))
+    codes = (np.floor(y.astype(np.float64) * 65536).astype(np.int64) + draw.astype(np.int64)) >> 16
+    return u, s, codes

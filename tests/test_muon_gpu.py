@@ -140,6 +140,100 @@ def test_strided_views(mua, count, rows, cols, kind):
         assert torch.equal(x, dense)
 
 
+def exact_on_gpu(x, steps=5):
+    """The definition in fp64 for a larger matrix, and a bound as muon_ref's with
+    the gains of the whole interval [0, s_max] of each step."""
+    y = x.double()
+    y = y / (y.norm() + 1e-7)
+    wide = y.shape[0] <= y.shape[1]
+    a, b, c = muon_ref.QUINTIC
+    gram = lambda v: v @ v.t() if wide else v.t() @ v  # noqa: E731
+    s = torch.linalg.eigvalsh(gram(y)).clamp_min(0).sqrt().cpu().numpy()
+    for _ in range(steps):
+        g = gram(y)
+        p = b * g + c * (g @ g)
+        y = a * y + (p @ y if wide else y @ p)
+    err = muon_ref.U16
+    for k in range(steps):
+        grid = np.linspace(0, s.max(), 4001)
+        gain = max(np.abs(a + 3 * b * grid ** 2 + 5 * c * grid ** 4).max(),
+                   np.abs(a + b * grid ** 2 + c * grid ** 4).max())
+        pol = a + b * s ** 2 + c * s ** 4
+        err = gain * err + muon_ref.U16 * s.max() * (
+            np.sqrt((s ** 4).sum()) * (abs(b) + 2 * abs(c) * s.max() ** 2)
+            + np.sqrt((pol ** 2).sum()))
+        s = np.abs(s * pol)
+        err += muon_ref.U16 * np.sqrt((s ** 2).sum())
+    return y, 1.25 * err
+
+
+# Shapes that take the other ways through the products: a shared contraction
+# (few tiles of A), pairs of CTAs on 256-wide tiles with ragged edges, several
+# tiles for each CTA, and both with the long side down.
+@pytest.mark.parametrize("count,rows,cols", [
+    (1, 200, 8000), (1, 8000, 200), (2, 129, 5000), (1, 520, 3000), (1, 3000, 520),
+    (1, 2100, 2300), (1, 2300, 2100), (14, 700, 900), (14, 900, 700), (1, 1, 11008),
+    (1, 11008, 1), (3, 24, 4000), (3, 4000, 24), (1, 128, 700), (1, 700, 128), (2, 64, 1500),
+    (200, 140, 150), (300, 16, 16)])
+def test_larger_shapes(mua, count, rows, cols):
+    x = randn(count, rows, cols, seed=rows + cols, dtype=torch.bfloat16)
+    out = ortho(mua, x)
+    for i in {0, count // 2, count - 1}:
+        want, bound = exact_on_gpu(x[i])
+        off = (out[i].double() - want).norm()
+        assert float(off) <= bound + UBF * float(want.norm())
+        # what fp16 operands give in practice (1e-3) and the result's own rounding
+        assert float(off) <= 5e-3 * float(want.norm())
+    again = ortho(mua, x)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("pk", ["f32", "bf16"])
+@pytest.mark.parametrize("count,rows,cols", [(1, 300, 6000), (16, 513, 770), (1, 2100, 1900)])
+def test_step_on_larger_shapes(mua, count, rows, cols, pk):
+    m = mua.Muon(rows, cols, count, bits=4)
+    st, ws = m.new_state(), m.new_workspace()
+    ref = st.clone()
+    p = randn(m.d, seed=6, scale=0.02, dtype=DT[pk])
+    before = p.double().view(count, rows, cols).clone()
+    g = randn(m.d, seed=2, dtype=torch.bfloat16)
+    u = torch.empty(m.d, device="cuda")
+    m.momentum(g, ref, u, beta=0.95, t=1, seed=9)
+    m.step(p, g, st, ws, lr=0.02, scale=1.5, wd=0.1, t=1, seed=9)
+    assert torch.equal(st, ref) and m.status(st) == 0
+    for i in {0, count - 1}:
+        o, bound = exact_on_gpu(u.view(count, rows, cols)[i])
+        want = before[i] * (1 - 0.02 * 0.1) - 0.03 * o
+        off = float((p.view(count, rows, cols)[i].double() - want).norm())
+        slack = 4 * U32 * float(before[i].norm())
+        assert off <= 0.03 * bound + slack + (UBF * float(want.norm()) if pk == "bf16" else 0)
+        if pk == "f32":
+            assert off <= 0.03 * 3e-3 * float(o.norm()) + slack
+
+
+def test_offsets_past_32_bits(mua):
+    """A state of more than 2^31 values: the last matrix's momentum, and a view
+    whose matrices lie more than 2^31 values apart."""
+    rows, cols = 11008, 4096
+    count = (1 << 31) // (rows * cols) + 2
+    m = mua.Muon(rows, cols, count, bits=4)
+    st = m.new_state()
+    n = rows * cols
+    g = torch.zeros(m.d, dtype=torch.bfloat16, device="cuda")
+    g[-n:] = randn(n, seed=3, dtype=torch.bfloat16)
+    u = torch.empty(m.d, dtype=torch.bfloat16, device="cuda")
+    m.momentum(g, st, u, beta=0.0, nesterov=False, t=1, seed=5)
+    assert torch.equal(u[-n:], g[-n:]) and torch.count_nonzero(u[:n]) == 0
+    u.zero_()
+    m.read_momentum(st, u)
+    step = g[-n:].float().view(-1, 128).abs().amax(1, keepdim=True) / 7
+    # one level of stochastic rounding and the bf16 rounding of the result
+    off = (u[-n:].float() - g[-n:].float()).view(-1, 128).abs()
+    assert (off <= step * (1 + 8 * UBF)).all() and torch.count_nonzero(u[:n]) == 0
+    far = torch.as_strided(g, (2, 60, 80), ((1 << 31) + 16, 96, 1), m.d - (1 << 31) - 16 - 59 * 96 - 80)
+    assert torch.equal(ortho(mua, far)[1], ortho(mua, far[1].contiguous())[0])
+
+
 def test_groups_of_a_large_stack(mua):
     """A stack that runs in several groups gives each matrix its own result."""
     x = randn(70, 700, 520, seed=12, dtype=torch.bfloat16)
@@ -199,6 +293,33 @@ def test_momentum(mua, count, rows, cols, bits, gk, dk):
         assert ((q2 >= np.maximum(lo, -level)) & (q2 <= np.minimum(hi, level)))[inside].all()
         assert (q2[~inside] == 0).all()
     assert m.status(st) == 0
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("count,rows,cols", [(1, 1, 1), (3, 77, 53), (2, 128, 96)])
+def test_state_bit_for_bit(mua, count, rows, cols, bits):
+    """Codes, scales and direction are those of fp32 with one rounding for each
+    operation, in the update alone and in the step."""
+    m = mua.Muon(rows, cols, count, bits=bits)
+    level, n = 2 ** (bits - 1) - 1, rows * cols
+    st, ws = random_state(m, bits, 14), m.new_workspace()
+    twin, p = st.clone(), torch.zeros(m.d, device="cuda")
+    inside = muon_ref.blocks_of(np.ones((count, n))) > 0
+    for t, nesterov in ((3, True), (4, False)):
+        q, s = muon_ref.unpack(st.cpu().numpy(), m.layout, count, n, bits)
+        g = randn(m.d, seed=t, scale=0.3)
+        u = torch.empty(m.d, device="cuda")
+        m.momentum(g, st, u, beta=0.95, nesterov=nesterov, t=t, seed=11)
+        m.step(p, g, twin, ws, lr=0.1, beta=0.95, nesterov=nesterov, t=t, seed=11)
+        gb = muon_ref.blocks_of(g.cpu().numpy().reshape(count, n))
+        want = muon_ref.momentum_f32(q, s, gb, 0.95, nesterov,
+                                     muon_ref.draws(count * m.layout.blocks, t, 11), level)
+        q2, s2 = muon_ref.unpack(st.cpu().numpy(), m.layout, count, n, bits)
+        got = muon_ref.blocks_of(u.cpu().numpy().reshape(count, n))
+        assert np.array_equal(got[inside], want[0][inside])
+        assert np.array_equal(s2, want[1])
+        assert np.array_equal(q2[inside], want[2][inside])
+        assert torch.equal(st, twin)
 
 
 @pytest.mark.parametrize("bits", [8, 4])
