@@ -397,6 +397,11 @@ int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t 
     return MUA_ERR_ARG;
   if (!aligned(x, type_size(x_type)) || !aligned(out, 2) || !aligned(workspace, 16))
     return MUA_ERR_ALIGN;
+  const bool same = out == x && x_type == MUA_BF16 && out_row_stride == x_row_stride &&
+                    (h->count == 1 || out_matrix_stride == x_matrix_stride);
+  const int64_t x_span = last * x_matrix_stride + (h->rows - 1) * x_row_stride + row;
+  const int64_t out_span = last * out_matrix_stride + (h->rows - 1) * out_row_stride + row;
+  if (!same && overlap(x, x_span * type_size(x_type), out, out_span * 2)) return MUA_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   double* partials = reinterpret_cast<double*>(ws + h->off_partials);
@@ -437,6 +442,10 @@ int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* g
   if (!aligned(params, type_size(params_type)) || !aligned(grads, type_size(grads_type)) ||
       !aligned(state, 16) || !aligned(workspace, 16))
     return MUA_ERR_ALIGN;
+  const int64_t all = (int64_t)h->rows * h->cols * h->count;
+  if (overlap(params, all * type_size(params_type), grads, all * type_size(grads_type)) ||
+      overlap(state, h->state_bytes, workspace, h->workspace_bytes))
+    return MUA_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   double* partials = reinterpret_cast<double*>(ws + h->off_partials);

@@ -74,6 +74,7 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
     if (split == 0 && threadIdx.x == 0) {
       factor[mat] = ns.factor;
       counters[mat] = 0;
+      if (isnan(ns.factor)) atomicOr(Q.status, kMuonNonFinite);
     }
   }
   bool bad = false;

@@ -21,10 +21,19 @@
 // warps 2..9 write finished accumulators out, through shared memory into whole
 // lines, while the next tile's MMAs run into the other half of TMEM, and warp 11
 // brings the addend of P in and counts finished tiles, so that nothing else
-// stands still for those. The instructions between two slices' MMAs are
-// what bounds the rate next to the tensor cores (256 cycles of MMA a slice on
-// 128 x 128, 512 on 256 x 256): hence a warp for each operand, one copy for an
+// stands still for those.
+//
+// A slice takes 512 cycles of MMA on 256 x 256 and 256 on 128 x 128, and in both
+// cases 32 KB a SM, 512 cycles at the 64 bytes a cycle that L2 delivers: the
+// large tile is bound by both at once, the small one by the copies. The way
+// through one slice's instructions (about 400 cycles in a producer, 430 in the
+// issuing warp) comes close: hence a warp for each operand, one copy for an
 // operand whose rows are contiguous in depth, and majors fixed per item.
+// Between two products of one matrix lie some 8000 cycles: a finished tile's
+// way to memory, its count and the next one's first copy.
+// Measured: 4096 x 4096, five steps, 1.0 ms on the device (1.36e12 operations of
+// the halved symmetric products and the updates; at the chip's power limit,
+// where cuBLAS keeps 1.39e15 a second); 768 x 768 0.11 ms, 48 of them 0.52 ms.
 //
 // Every wait is bounded by the global timer. A wait that runs out sets
 // MUA_STATUS_TIMEOUT, the CTA's roles stop, copies and MMAs in flight are

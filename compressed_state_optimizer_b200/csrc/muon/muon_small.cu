@@ -302,7 +302,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
         }
       }
     }
-    if (bad) atomicOr(Q.status, kMuonNonFinite);
+    if (bad || (threadIdx.x == 0 && isnan(ns.factor))) atomicOr(Q.status, kMuonNonFinite);
   }
   fence_async_shared();
   fence_before();

@@ -49,18 +49,35 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// Whether the phase is over, without waiting (a try may suspend the thread).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // False when the wait ran out, or another role of the CTA has given up. The
 // timer is read once in 1024 tries: a read takes longer than most waits. A
-// limit of 0 gives up as soon as it would wait.
+// limit of 0 gives up where it would wait.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit,
                                           volatile uint32_t* stop) {
+  if (limit == 0) {
+    if (mbar_test(bar, parity)) return true;
+    *stop = 1;
+    return false;
+  }
   uint64_t t0 = 0;
   for (uint32_t n = 1; !mbar_try(bar, parity); ++n) {
-    if (limit != 0 && (n & 1023u) != 0) continue;
+    if ((n & 1023u) != 0) continue;
     if (*stop) return false;
     const uint64_t t = now_ns();
     if (t0 == 0) t0 = t;
-    if (limit == 0 || t - t0 > limit) {
+    if (t - t0 > limit) {
       *stop = 1;
       return false;
     }
@@ -70,7 +87,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
 // The same for a converged warp: one answer for all lanes.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit,
                                                volatile uint32_t* stop) {
-  if (__all_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return true;
+  if (limit != 0 && __all_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return true;
   const bool ok = mbar_wait(bar, parity, limit, stop);
   return __all_sync(0xFFFFFFFFu, ok);
 }

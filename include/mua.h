@@ -271,9 +271,9 @@ int mua_get_status(mua_t h, const void* state, void* stream, int32_t* out);
  * at once when they use different states and workspaces; a workspace belongs
  * to one call at a time (captured graphs that share one must not overlap).
  * Pointers to values need the alignment of their type, states and workspaces
- * 16 bytes. A NaN or infinity in m' sets MUA_STATUS_NONFINITE in the state and
- * makes that matrix's results NaN or unspecified; other matrices are not
- * affected. MUA_ERR_CUDA's text is given by mua_muon_last_cuda_error().
+ * 16 bytes. A NaN or infinity in m', or in a step's U, sets
+ * MUA_STATUS_NONFINITE in the state and makes that matrix's results NaN or
+ * unspecified; other matrices are not affected. MUA_ERR_CUDA's text is given by mua_muon_last_cuda_error().
  */
 #define MUA_F32 0  /* types of values */
 #define MUA_BF16 1
@@ -342,8 +342,9 @@ int mua_muon_write(mua_muon_t h, const void* values, int32_t type, void* state, 
  * mua_muon_orthogonalize - X_steps of a stack of matrices x, to the bf16 stack
  * out. Strides count elements; columns are contiguous. x may be broadcast
  * (stride 0); the rows of out must not overlap. out may be x itself (bf16, the
- * same strides), but may not overlap it otherwise. eps >= 0. A matrix of zeros
- * gives zeros; one with a NaN or infinity gives NaN.
+ * same strides); otherwise the two address ranges must not overlap
+ * (MUA_ERR_ARG). eps >= 0. A matrix of zeros gives zeros; one with a NaN or
+ * infinity gives NaN.
  */
 int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t x_matrix_stride,
                            int64_t x_row_stride, void* out, int64_t out_matrix_stride,
@@ -352,7 +353,8 @@ int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t 
 /*
  * mua_muon_step - the whole step t (1, 2, ...) on `stream`: params (fp32 or
  * bf16, contiguous) are updated in place, formed in fp32 and rounded once.
- * X_steps is not rounded to bf16 on the way.
+ * X_steps is not rounded to bf16 on the way. params and grads, state and
+ * workspace must not overlap (MUA_ERR_ARG).
  */
 int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* grads,
                   int32_t grads_type, void* state, void* workspace, float lr, float scale,

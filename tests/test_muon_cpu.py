@@ -135,12 +135,14 @@ def step(h=h, p=a, pt=0, g=b, gt=1, s=c, w=d, lr=0.1, scale=1.0, beta=0.9, eps=1
     ("orth(xt=5)", -1), ("orth(eps=-1.0)", -1), ("orth(eps=nan)", -1), ("orth(eps=inf)", -1),
     ("orth(xm=-1)", -1), ("orth(xr=-10)", -1), ("orth(orow=9)", -1), ("orth(om=0)", -1),
     ("orth(om=59)", -1), ("orth(om=10, orow=19)", -1), ("orth(x=odd)", -3), ("orth(o=odd)", -3),
-    ("orth(w=P(0x30008))", -3),
+    ("orth(w=P(0x30008))", -3), ("orth(o=a)", -1), ("orth(o=P(0x10000 + 100))", -1),
+    ("orth(xt=1, o=P(0x10000 + 2))", -1), ("orth(xt=1, o=a, xm=0)", -1),
     ("step(h=None)", -1), ("step(p=None)", -1), ("step(g=None)", -1), ("step(s=None)", -1),
     ("step(w=None)", -1), ("step(pt=3)", -1), ("step(gt=3)", -1), ("step(t=0)", -1),
     ("step(lr=nan)", -1), ("step(scale=inf)", -1), ("step(beta=-0.1)", -1), ("step(eps=-1e-9)", -1),
     ("step(wd=nan)", -1), ("step(p=odd)", -3), ("step(g=odd)", -3), ("step(s=P(0x30004))", -3),
-    ("step(w=P(0x40008))", -3),
+    ("step(w=P(0x40008))", -3), ("step(g=a)", -1), ("step(w=c)", -1),
+    ("step(g=P(0x10000 + 476))", -1), ("step(w=P(0x30000 + 256))", -1),
     ("lib.mua_muon_read(h, None, a, 0, None)", -1), ("lib.mua_muon_read(h, a, b, 7, None)", -1),
     ("lib.mua_muon_read(h, P(0x10004), b, 0, None)", -3),
     ("lib.mua_muon_write(h, None, 0, a, None)", -1), ("lib.mua_muon_write(h, odd, 1, b, None)", -3),

@@ -420,6 +420,17 @@ def test_nonfinite_status(mua, value):
     assert m.status(st2) == 0 and torch.equal(p[600:], q[600:])  # the other matrix
 
 
+@pytest.mark.parametrize("rows,cols", [(20, 30), (200, 300)])
+def test_direction_overflow_status(mua, rows, cols):
+    """m' is finite and U is not: the step says so."""
+    m = mua.Muon(rows, cols)
+    g = torch.zeros(m.d, device="cuda")
+    g[5] = 3e38
+    st, p = m.new_state(), torch.zeros(m.d, device="cuda")
+    m.step(p, g, st, m.new_workspace(), lr=0.1, beta=0.9, t=1, seed=1)
+    assert m.status(st) == mua.MUA_STATUS_NONFINITE and p.isnan().all()
+
+
 # ------------------------------------------------------------ the step
 @pytest.mark.parametrize("pk,gk,bits", [("f32", "bf16", 8), ("bf16", "bf16", 4),
                                         ("f32", "f32", 4), ("bf16", "f32", 8)])
@@ -533,13 +544,15 @@ def test_streams_graphs_and_reruns(mua, count, rows, cols):
         assert torch.equal(p, want) and torch.equal(s, st)
 
 
-def test_wait_limit_sets_timeout(mua):
+@pytest.mark.parametrize("count,rows,cols", [(1, 300, 700), (1, 64, 64), (2, 200, 5000),
+                                             (20, 700, 513)])
+def test_wait_limit_sets_timeout(mua, count, rows, cols):
     """With a limit of 0 the product kernels give up at their first wait, end,
     and say so; the next call with the default limit is right."""
-    x = randn(1, 300, 700, seed=4)
-    m = mua.Muon(300, 700)
+    x = randn(count, rows, cols, seed=4)
+    m = mua.Muon(rows, cols, count)
     ws = m.new_workspace()
-    out = torch.empty((1, 300, 700), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty((count, rows, cols), dtype=torch.bfloat16, device="cuda")
     m.set_wait_limit_ns(0)
     m.orthogonalize(x, out, ws)
     assert m.status(ws) & mua.MUA_STATUS_TIMEOUT
@@ -547,7 +560,7 @@ def test_wait_limit_sets_timeout(mua):
     ws[:256].zero_()
     m.orthogonalize(x, out, ws)
     assert m.status(ws) == 0
-    check_ortho(x, out)
+    assert torch.equal(out, ortho(mua, x))
 
 
 def test_refusals_on_gpu(mua):
