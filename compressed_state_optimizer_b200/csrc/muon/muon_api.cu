@@ -284,7 +284,7 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
   h->tiling = wide.us <= narrow.us ? wide : narrow;
   // The norm's sums: four CTAs an SM of a B200 in all, 8192 values each or more.
   h->parts = (int32_t)std::max<int64_t>(
-      1, std::min<int64_t>((4 * 148 + h->group - 1) / h->group, n / 8192));
+      1, std::min<int64_t>(4 * 148 / h->group, n / 8192));
   int64_t at = 256;
   auto take = [&at](int64_t bytes) {
     const int64_t o = at;

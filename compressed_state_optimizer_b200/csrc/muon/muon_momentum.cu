@@ -4,8 +4,13 @@
 //
 // Half a warp holds a block, 8 values per lane: a 16-byte load of bf16
 // gradients (two for fp32), one 8- or 4-byte load of codes, one Philox call
-// per lane; the block maximum is four shuffles. Bound by HBM: nothing is
-// read twice, and U is formed from the unrounded m' in the same pass.
+// per lane; the block maximum is four shuffles. Nothing is read twice, and U is
+// formed from the unrounded m' in the same pass. Of 6.06 bytes a value (bf16
+// gradients and direction, 8 bits) HBM would take 0.34 ms for 8 x 11008 x 4096;
+// the update takes 0.55 ms, bound by its 38 instructions a value (a fifth of
+// them Philox, the rest the conversions, the clamp and the packing) at 2.3
+// instructions a cycle; packed fp32 pairs and the next run's loads in flight
+// brought it there from 0.96 ms. Reading back runs at HBM's rate (0.17 ms).
 #include "muon_quant.cuh"
 
 #include <algorithm>
@@ -332,11 +337,12 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, cudaStream_t st, bool ove
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-// CTAs a matrix is split over: about eight for each SM of a B200 in all, as each
-// begins with the norm's sum, and none without work.
+// CTAs a matrix is split over: eight for each SM of a B200 in all, and none
+// without work. Four run at once; twice as many even out their ends (592 CTAs
+// take 0.64 ms for the update of 8 x 11008 x 4096, 1184 0.55 ms, 4736 0.57 ms).
 int splits_for(int count, int64_t work, int64_t per_cta) {
   const int64_t most = (work + per_cta - 1) / per_cta;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(most, (8 * 148 + count - 1) / count));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, 8 * 148 / count));
 }
 
 int64_t chunk_splits(const MuonQuant& q) { return (q.bpm + kChunkBlocks - 1) / kChunkBlocks; }
