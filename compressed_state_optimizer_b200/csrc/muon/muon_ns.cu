@@ -416,39 +416,41 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
   } else if (warp == 1) {
     if (rank == 0) {
       uint32_t n = 0, s = 0, turn = 0;
-      bool ok = true;
+      bool ok = true, ready = false;  // the next slice, of whichever item, has landed
+      const bool elected = elect_one();
       for (Walk<BN> walk(g, first, stride); ok && walk.more(); walk.advance()) {
         if (walk.kind == kReduce) continue;
         const Item it = walk.item();
         const uint32_t acc = n & 1u;
-        ok = mbar_wait(smem_u32(&acc_empty[acc]), ((n >> 1) & 1u) ^ 1u, g.wait_ns, stop_v);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        fence_after();
         const uint32_t d = tmem + acc * BN;
         const int a_from = first_mn<BN>(g, it, true), b_from = first_mn<BN>(g, it, false);
+        ok = mbar_wait_warp(smem_u32(&acc_empty[acc]), ((n >> 1) & 1u) ^ 1u, g.wait_ns, stop_v);
+        if (!ok) break;
+        fence_after();
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
           const uint32_t a = ring + s * kStageBytes, b = a + kOperandBytes;
           const bool a_mn = kb >= a_from, b_mn = kb >= b_from;
           const uint32_t idesc = instruction_desc<CG>(BN, a_mn, b_mn);
           const uint64_t da = operand_desc(a, 8192), db = operand_desc(b, 8192);
-          const uint64_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
-          ok = mbar_wait_warp(smem_u32(&full[s]), turn, g.wait_ns, stop_v);
+          const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+          if (!ready) ok = mbar_wait_warp(smem_u32(&full[s]), turn, g.wait_ns, stop_v);
           if (!ok) break;
           fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16<CG>(d, da + k * sa, db + k * sb, idesc, kb != it.kb0 || k != 0);
-            mma_commit<CG>(smem_u32(&empty[s]));
-          }
-          __syncwarp();
+          const uint32_t done = smem_u32(&empty[s]);
           if (++s == S) {
             s = 0;
             turn ^= 1u;
           }
+          // Asked before the MMAs go out, answered behind them.
+          const bool landed = mbar_test(smem_u32(&full[s]), turn);
+          if (elected) {
+            mma_slice<CG>(d, (uint32_t)da, (uint32_t)db, (uint32_t)(da >> 32), sa, sb, idesc,
+                          kb != it.kb0);
+            mma_commit<CG>(done);
+          }
+          ready = __all_sync(0xFFFFFFFFu, landed);
         }
-        if (ok && elect_one()) mma_commit<CG>(smem_u32(&acc_full[acc]));
+        if (ok && elected) mma_commit<CG>(smem_u32(&acc_full[acc]));
         __syncwarp();
         ++n;
       }

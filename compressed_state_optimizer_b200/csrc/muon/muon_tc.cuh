@@ -177,6 +177,32 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
+// The four MMAs of a 64-deep slice: low words of the operands' descriptors, their
+// steps, and the high word both share.
+template <int CG>
+__device__ __forceinline__ void mma_slice(uint32_t d, uint32_t a, uint32_t b, uint32_t high,
+                                          uint32_t a_step, uint32_t b_step, uint32_t idesc,
+                                          bool accumulate) {
+#define MUA_MMA_SLICE(G)                                                                        \
+  asm volatile(                                                                                 \
+      "{\n .reg .pred p, q;\n .reg .b32 x, y;\n .reg .b64 u, v;\n"                              \
+      " setp.ne.b32 p, %7, 0;\n setp.eq.b32 q, 0, 0;\n"                                         \
+      " mov.b64 u, {%1, %3};\n mov.b64 v, {%2, %3};\n"                                          \
+      " tcgen05.mma.cta_group::" G ".kind::f16 [%0], u, v, %6, p;\n"                            \
+      " add.u32 x, %1, %4;\n add.u32 y, %2, %5;\n mov.b64 u, {x, %3};\n mov.b64 v, {y, %3};\n"  \
+      " tcgen05.mma.cta_group::" G ".kind::f16 [%0], u, v, %6, q;\n"                            \
+      " add.u32 x, x, %4;\n add.u32 y, y, %5;\n mov.b64 u, {x, %3};\n mov.b64 v, {y, %3};\n"    \
+      " tcgen05.mma.cta_group::" G ".kind::f16 [%0], u, v, %6, q;\n"                            \
+      " add.u32 x, x, %4;\n add.u32 y, y, %5;\n mov.b64 u, {x, %3};\n mov.b64 v, {y, %3};\n"    \
+      " tcgen05.mma.cta_group::" G ".kind::f16 [%0], u, v, %6, q;\n}\n" ::"r"(d),               \
+      "r"(a), "r"(b), "r"(high), "r"(a_step), "r"(b_step), "r"(idesc), "r"((uint32_t)accumulate) \
+      : "memory")
+  if constexpr (CG == 2)
+    MUA_MMA_SLICE("2");
+  else
+    MUA_MMA_SLICE("1");
+#undef MUA_MMA_SLICE
+}
 // Arrives on the barrier (of both CTAs of a pair) when the MMAs issued so far are done.
 template <int CG>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
