@@ -11,9 +11,10 @@
 // in fp16 (11 significant bits) with a power of two that the host derives
 // from a bound on their spectral norms, so that no entry overflows and an
 // entry is subnormal only when it is 2^-28 of that bound; every product and
-// norm is summed in fp32 or fp64. Against fp64, for a Gaussian matrix of
-// 768 x 768: 1.2e-3 relative in the Frobenius norm (bf16 operands: 1.0e-2;
-// the final rounding to bf16 alone: 1.7e-3).
+// norm is summed in fp32 or fp64. Against fp64, simulated for a Gaussian matrix
+// of 768 x 768: 1.2e-3 relative in the Frobenius norm (bf16 operands: 1.0e-2;
+// the final rounding to bf16 alone: 1.7e-3). Matrices that stay on one SM hold A
+// and P as two fp16 values each: 0.5e-3.
 #pragma once
 
 #include <cstdint>

@@ -3,6 +3,12 @@
 // MMAs read (128-byte swizzled rows of 64 elements), accumulators in TMEM;
 // global memory is read once or twice at the start and written once at the end.
 //
+// A and P are held as two fp16 tiles each, a value and what its rounding left
+// (P's take A's place): A A is then three products and P X two. That costs
+// 64 x 64 20.5 us instead of 16.8, 16 x 768 with a step around it 30.6 instead of
+// 28.7, 128 x 512 74 instead of 65; a small matrix, whose few roundings do not
+// average out, comes to 0.5e-3 of the exact result instead of 1e-3 to 3e-3.
+//
 // Each of the 3 products per step is a handful of MMAs, issued by a warp of
 // their own, followed by an epilogue of the 16 others, so a step is bound by the
 // latency of issue, completion, TMEM read and the hand-over, not by arithmetic.
@@ -32,8 +38,8 @@ struct Plan {
   int s, l, s16, l16;     // short and long side, padded
   bool tall;              // rows > cols
   int ns, chunks;         // 64-wide chunks of the short side; of X
-  uint32_t xs;            // bytes of a chunk of X, A and P: s16 rows of 128
-  uint32_t a_off, p_off, bytes;
+  uint32_t xs;            // bytes of a chunk: s16 rows of 128
+  uint32_t hi_off, lo_off, bytes;  // of A's and P's two tiles; all
   uint32_t columns;       // of TMEM
 };
 __host__ __device__ __forceinline__ Plan plan_of(int rows, int cols) {
@@ -46,9 +52,9 @@ __host__ __device__ __forceinline__ Plan plan_of(int rows, int cols) {
   p.ns = (p.s + 63) / 64;
   p.chunks = (p.l + 63) / 64;
   p.xs = (uint32_t)p.s16 * 128u;
-  p.a_off = (uint32_t)p.chunks * p.xs;
-  p.p_off = p.a_off + (uint32_t)p.ns * p.xs;
-  p.bytes = p.p_off + (uint32_t)p.ns * p.xs + kOverread;
+  p.hi_off = (uint32_t)p.chunks * p.xs;
+  p.lo_off = p.hi_off + (uint32_t)p.ns * p.xs;
+  p.bytes = p.lo_off + (uint32_t)p.ns * p.xs + kOverread;
   const int update = (p.l + 127) / 128 * p.s16;
   const int need = update > 512 ? 512 : (update > p.s16 ? update : p.s16);
   p.columns = 32;
@@ -68,6 +74,42 @@ __device__ __forceinline__ uint32_t value_address(uint32_t X, uint32_t xs, int j
 }
 __device__ __forceinline__ void st_half(uint32_t at, uint32_t bits) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)bits) : "memory");
+}
+
+// Columns col .. col + 15 of a row, in fp16, and what that rounding left of them.
+__device__ __forceinline__ void store_split(uint32_t hi, uint32_t lo, uint32_t xs, int row, int col,
+                                            const float (&x)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x0 = x[8 * h + 2 * e], x1 = x[8 * h + 2 * e + 1];
+      a[e] = pack_f16(x0, x1);
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&a[e]));
+      b[e] = pack_f16(x0 - y.x, x1 - y.y);
+    }
+    st_shared(group_address(hi, xs, row, col + 8 * h), a[0], a[1], a[2], a[3]);
+    st_shared(group_address(lo, xs, row, col + 8 * h), b[0], b[1], b[2], b[3]);
+  }
+}
+
+// The 16 values again, to 22 bits.
+__device__ __forceinline__ void load_split(uint32_t hi, uint32_t lo, uint32_t xs, int row, int col,
+                                           float (&x)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 u = ld_shared(group_address(hi, xs, row, col + 8 * h));
+    const uint4 w = ld_shared(group_address(lo, xs, row, col + 8 * h));
+    const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&a[e]));
+      const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&b[e]));
+      x[8 * h + 2 * e] = y.x + z.x;
+      x[8 * h + 2 * e + 1] = y.y + z.y;
+    }
+  }
 }
 
 // The last product's 16 values of a lane, `left` of them inside the matrix, in
@@ -133,7 +175,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
   __shared__ NormScale scale_s;
   const Plan p = plan_of(sh.rows, sh.cols);
   const uint32_t X = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t A = X + p.a_off, P = X + p.p_off;
+  const uint32_t hi = X + p.hi_off, lo = X + p.lo_off;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t mat = blockIdx.x;
   const int64_t n = (int64_t)sh.rows * sh.cols;
@@ -155,7 +197,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
   }
   // Rows and columns that pad a side to 16 hold zeros throughout.
   if (((p.s | p.l) & 15) != 0)
-    for (uint32_t o = threadIdx.x * 16; worker && o < p.a_off; o += kWorkers * 16)
+    for (uint32_t o = threadIdx.x * 16; worker && o < p.hi_off; o += kWorkers * 16)
       st_shared(X + o, 0u, 0u, 0u, 0u);
 
   // The norm, then X_0 = x 2^(e0 - t): see muon_launch_load.
@@ -320,13 +362,13 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     const bool lead = elect_one();
     const uint32_t sym = instruction_desc<1>(p.s16, false, false);
     const uint32_t upd = instruction_desc<1>(p.s16, true, false);
-    const uint64_t x0 = operand_desc(X, 16), a0 = operand_desc(A, 16), p0 = operand_desc(P, 16);
+    const uint64_t x0 = operand_desc(X, 16), h0 = operand_desc(hi, 16), l0 = operand_desc(lo, 16);
     const uint64_t xt = operand_desc(X, p.xs);  // X by its columns
     const uint32_t chunk = p.xs >> 4;
     // `depth` k-steps of 16 along the rows of two operands.
-    auto along = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int depth) {
+    auto along = [&](uint64_t a, uint64_t b, int depth, bool more) {
       for (int kk = 0; kk < depth; ++kk) {
-        if (lead) mma_f16<1>(d, a, b, idesc, kk != 0);
+        if (lead) mma_f16<1>(tmem, a, b, sym, more || kk != 0);
         const uint32_t step = (kk & 3) == 3 ? chunk - 6 : 2;
         a += step;
         b += step;
@@ -341,10 +383,12 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     };
     for (int k = 0; ok && k < g.steps; ++k) {
       if (!begin()) break;
-      along(tmem, x0, x0, sym, p.l16 / 16);  // X X^T
+      along(x0, x0, p.l16 / 16, false);  // X X^T
       if (lead) mma_commit<1>(smem_u32(&done));
       if (!begin()) break;
-      along(tmem, a0, a0, sym, sunits);      // A A
+      along(h0, h0, sunits, false);      // A A without its low parts' product
+      along(h0, l0, sunits, true);
+      along(l0, h0, sunits, true);
       if (lead) mma_commit<1>(smem_u32(&done));
       for (int t0 = 0; t0 < tiles; t0 += pass) {
         if (!begin()) break;
@@ -352,11 +396,16 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
         uint64_t a_tile = xt + (uint32_t)t0 * 2 * chunk;
         const int now = min(pass, tiles - t0);
         for (int t = 0; t < now; ++t, a_tile += 2 * chunk) {
-          uint64_t a = a_tile, b = p0;
+          uint64_t a = a_tile, b = h0, c = l0;
           for (int kk = 0; kk < sunits; ++kk) {
-            if (lead) mma_f16<1>(tmem + t * p.s16, a, b, upd, kk != 0);
+            if (lead) {
+              mma_f16<1>(tmem + t * p.s16, a, b, upd, kk != 0);
+              mma_f16<1>(tmem + t * p.s16, a, c, upd, true);
+            }
             a += 2048 >> 4;
-            b += (kk & 3) == 3 ? chunk - 6 : 2;
+            const uint32_t step = (kk & 3) == 3 ? chunk - 6 : 2;
+            b += step;
+            c += step;
           }
         }
         if (lead) mma_commit<1>(smem_u32(&done));
@@ -385,7 +434,6 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     for (int k = 0; k < g.steps; ++k) {
       // A = f^2 X X^T
       if (!take()) break;
-      uint32_t held[2][8];  // this thread's part of A, for the next product
       if (quarter * 32 < p.s16) {
         const float alpha = k == 0 ? g.gram_alpha[0] * factor * factor : g.gram_alpha[k];
 #pragma unroll
@@ -393,18 +441,12 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
           const int u = part + 4 * q;
           if (u < sunits) {
             uint32_t v[16];
+            float x[16];
             tmem_load16(lanes + 16 * u, v);
             tmem_load_wait();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              held[q][e] = pack_f16(__uint_as_float(v[2 * e]) * alpha,
-                                    __uint_as_float(v[2 * e + 1]) * alpha);
-            if (lane_row < p.s16) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                st_shared(group_address(A, p.xs, lane_row, 16 * u + 8 * h), held[q][4 * h],
-                          held[q][4 * h + 1], held[q][4 * h + 2], held[q][4 * h + 3]);
-            }
+            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]) * alpha;
+            if (lane_row < p.s16) store_split(hi, lo, p.xs, lane_row, 16 * u, x);
             __syncwarp();
           }
         }
@@ -423,21 +465,15 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
             tmem_load16(lanes + 16 * u, v);
             tmem_load_wait();
             const int diagonal = lane_row < p.s ? lane_row - 16 * u : -1;
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&held[q][e]));
-              float x0 = fmaf(y.x, mid, __uint_as_float(v[2 * e]) * alpha);
-              float x1 = fmaf(y.y, mid, __uint_as_float(v[2 * e + 1]) * alpha);
-              if (2 * e == diagonal) x0 += diag;
-              if (2 * e + 1 == diagonal) x1 += diag;
-              w[e] = pack_f16(x0, x1);
-            }
             if (lane_row < p.s16) {
+              float x[16];
+              load_split(hi, lo, p.xs, lane_row, 16 * u, x);  // of A: its own values
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                st_shared(group_address(P, p.xs, lane_row, 16 * u + 8 * h), w[4 * h], w[4 * h + 1],
-                          w[4 * h + 2], w[4 * h + 3]);
+              for (int e = 0; e < 16; ++e) {
+                x[e] = fmaf(x[e], mid, __uint_as_float(v[e]) * alpha);
+                if (e == diagonal) x[e] += diag;
+              }
+              store_split(hi, lo, p.xs, lane_row, 16 * u, x);
             }
             __syncwarp();
           }
