@@ -41,7 +41,7 @@ struct MuonView {
 
 struct MuonShape {
   int32_t rows, cols, count;  // count: matrices of this launch
-  int32_t ld;                 // row stride of the fp16 matrices X (cols up to a multiple of 8)
+  int32_t ld;                 // row stride of the fp16 matrices X
   int32_t parts;              // partial sums per matrix
 };
 

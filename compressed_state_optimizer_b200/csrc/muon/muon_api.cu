@@ -228,6 +228,14 @@ Tiling tiling(int32_t rows, int32_t cols, int32_t batch, int32_t bn) {
   return t;
 }
 
+// Row stride of an fp16 matrix in the workspace: rows start at 128-byte lines, or
+// fit one, so that a copy of 64 columns never takes a part of a second line
+// (1000 x 1000 at a stride of 1000: 158 us, 1024: 119; 3000 x 3000: 692, 550).
+int32_t row_stride(int32_t cols) {
+  if (cols > 32) return (int32_t)round_up(cols, 64);
+  return cols > 16 ? 32 : cols > 8 ? 16 : 8;
+}
+
 int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t steps,
            const float* coefficients, mua_muon_t* out) {
   if (!out) return MUA_ERR_ARG;
@@ -267,8 +275,8 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
   h->s = s;
   h->tall = rows > cols;
   h->small = mua::muon_small_smem(rows, cols) > 0;
-  h->ld = (int32_t)round_up(cols, 8);
-  h->lds = (int32_t)round_up(s, 8);
+  h->ld = row_stride(cols);
+  h->lds = row_stride(s);
   h->bpm = bpm;
   h->off_scales = 256;
   h->off_codes = h->off_scales + round_up(4 * count * bpm, 256);

@@ -104,11 +104,11 @@ momentum_kernel(MuonShape s, MuonQuant Q, const void* g, float beta, int nestero
       if constexpr (OUT == 2) {
         __half* x = static_cast<__half*>(X) + (int64_t)mat * s.rows * s.ld;
         const uint4 h = scaled_f16(u, ns.first, ns.second);
-        if ((s.cols & 7) == 0) {  // eight values of one row, and ld == cols
-          if (left > 0) *reinterpret_cast<uint4*>(x + i) = h;
+        const uint32_t row = s.ld == s.cols ? 0 : (uint32_t)i / (uint32_t)s.cols;
+        if ((s.cols & 7) == 0) {  // eight values of one row
+          if (left > 0) *reinterpret_cast<uint4*>(x + i + (int64_t)row * (s.ld - s.cols)) = h;
         } else {
           const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-          const uint32_t row = (uint32_t)i / (uint32_t)s.cols;
           uint32_t col = (uint32_t)i - row * (uint32_t)s.cols;
           uint16_t* at = reinterpret_cast<uint16_t*>(x) + (int64_t)row * s.ld + col;
 #pragma unroll
@@ -225,7 +225,7 @@ load_kernel(MuonShape s, MuonView x, const double* partials, float eps, int e0, 
   const int es = T == kBf16 ? 2 : 4;
   const uint8_t* xm = static_cast<const uint8_t*>(x.p) + mat * x.matrix_stride * es;
   const bool vec = aligned16(xm) && (x.row_stride * es) % 16 == 0;
-  const uint32_t per_row = (uint32_t)(s.ld / 8), groups = per_row * (uint32_t)s.rows;
+  const uint32_t per_row = (uint32_t)(s.cols + 7) / 8, groups = per_row * (uint32_t)s.rows;
   const NormScale ns = norm_scale(partials + (int64_t)mat * s.parts, s.parts, eps, e0);
   if (split == 0 && threadIdx.x == 0) {
     factor[mat] = ns.factor;
@@ -359,7 +359,7 @@ cudaError_t muon_launch_norm(const MuonShape& s, const MuonView& x, double* part
 cudaError_t muon_launch_load(const MuonShape& s, const MuonView& x, const double* partials,
                              float eps, int e0, void* X, float* factor, uint32_t* counters,
                              cudaStream_t st) {
-  const int splits = splits_for(s.count, (int64_t)s.rows * (s.ld / 8), kLoadUnroll * kThreads);
+  const int splits = splits_for(s.count, (int64_t)s.rows * ((s.cols + 7) / 8), kLoadUnroll * kThreads);
   const int64_t grid = (int64_t)s.count * splits;
   auto k = x.type == kBf16 ? load_kernel<kBf16> : load_kernel<kF32>;
   return launch(k, grid, st, true, s, x, partials, eps, e0, X, factor, counters, splits);
