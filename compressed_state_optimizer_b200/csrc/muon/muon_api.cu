@@ -193,17 +193,19 @@ int iterate(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count, co
 // Time of a step's products on tiles of bn, in us: per product the waves of
 // items over the SMs (whole ones for a single matrix; those of a stack overlap),
 // an item's k-slices and what it adds to them, and the way from one product's
-// last store to the next one's first MMA. Fitted to measurements: a 64-deep
-// slice takes 0.30 us on 256 x 256 tiles of CTA pairs and 0.28 us on 128 x 128
-// (32 KB an SM either way, the rate of L2), an item 2 and 0.7 us more, between
-// products 4.2 us. So the larger tile, with four times the work a slice, wins
-// from about 2048 x 2048 (245 against 249 us) or 8 x 1024 x 1024 (208, 224 us)
-// on, the smaller one where its items fit the SMs at once: 768 x 768 (108, 140),
-// 5 x 1000 x 333 (104, 139). Sharing A's tiles among idle SMs costs a product
-// more: 512 x 11008 343 -> 184 us, but 5 x 1000 x 333 104 -> 123 us.
+// last store to the next one's first MMA. Fitted to 36 shapes from 256 x 256 to
+// 4096 x 4096 and 148 x 256 x 256, each measured on both tiles: a 64-deep slice
+// takes 0.34 us on 256 x 256 tiles of CTA pairs and 0.23 us on 128 x 128, an item
+// 3.0 and 1.1 us more, between products 3.3 us; the choice is within 4 % of the
+// better tile on all of them. The larger one, with four times the work a slice,
+// wins where its items fill the SMs anyway: 4096 x 4096 (1154 against 1494 us),
+// 3000 x 3000 (545, 653), 24 x 768 x 768 (253, 316). The smaller one wins below:
+// 768 x 768 (102, 142), 2048 x 2048 (218, 241), 12 x 768 x 768 (159, 181).
+// Sharing A's tiles among idle SMs costs a product more: 512 x 11008 305 -> 187
+// us and 1024 x 4096 199 -> 183, but 1024 x 1024 115 -> 130 us.
 Tiling tiling(int32_t rows, int32_t cols, int32_t batch, int32_t bn) {
   const bool big = bn == 256;
-  const double slice = big ? 0.30 : 0.28, item = big ? 2.0 : 0.7, between = 4.2;
+  const double slice = big ? 0.34 : 0.23, item = big ? 3.0 : 1.1, between = 3.3;
   const int64_t units = big ? 74 : 148;  // CTA pairs or CTAs of a B200
   const int64_t s = std::min(rows, cols), l = std::max(rows, cols);
   const int64_t tm = (s + bn - 1) / bn, sym = tm * (tm + 1) / 2 * batch;

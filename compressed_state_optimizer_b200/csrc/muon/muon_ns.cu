@@ -33,7 +33,7 @@
 // way to memory, its count and the next one's first copy.
 // Measured: 4096 x 4096, five steps, 1.0 ms on the device (1.36e12 operations of
 // the halved symmetric products and the updates; at the chip's power limit,
-// where cuBLAS keeps 1.39e15 a second); 768 x 768 0.11 ms, 48 of them 0.52 ms.
+// where cuBLAS keeps 1.39e15 a second); 768 x 768 0.10 ms, 48 of them 0.5 ms.
 //
 // Every wait is bounded by the global timer. A wait that runs out sets
 // MUA_STATUS_TIMEOUT, the CTA's roles stop, copies and MMAs in flight are

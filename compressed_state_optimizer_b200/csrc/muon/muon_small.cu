@@ -9,6 +9,11 @@
 // 28.7, 128 x 512 74 instead of 65; a small matrix, whose few roundings do not
 // average out, comes to 0.5e-3 of the exact result instead of 1e-3 to 3e-3.
 //
+// What fits comes here: the general kernels, with their launches and their way
+// through L2 between products, take 51 us for 64 x 64 (here 20.5), 68 for 16 x 768
+// (27), 235 for 1000 x 64 x 64 (138). Only the longest that fit lose a little,
+// 128 x 512 (68, here 73), and stay for the smaller error.
+//
 // Each of the 3 products per step is a handful of MMAs, issued by a warp of
 // their own, followed by an epilogue of the 16 others, so a step is bound by the
 // latency of issue, completion, TMEM read and the hand-over, not by arithmetic.
