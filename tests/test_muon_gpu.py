@@ -211,6 +211,24 @@ def test_step_on_larger_shapes(mua, count, rows, cols, pk):
             assert off <= 0.03 * 3e-3 * float(o.norm()) + slack
 
 
+@pytest.mark.parametrize("count,rows,cols", [
+    (3, 9000, 40), (2, 12000, 24), (1, 20000, 8), (1, 9000, 9), (1, 40, 9000), (2, 200, 333),
+    (1, 333, 1000), (2, 513, 770)])
+def test_rows_that_end_inside_a_line(mua, count, rows, cols):
+    """The scratch matrices' rows are padded; whatever the padding holds (here
+    NaN), nothing of it is read."""
+    test_step_on_larger_shapes(mua, count, rows, cols, "f32")
+    m = mua.Muon(rows, cols, count)
+    x = randn(count, rows, cols, seed=cols)
+    clean, poisoned = m.new_workspace(), m.new_workspace()
+    clean.zero_()
+    poisoned[256:] = 255
+    out = torch.empty((2, count, rows, cols), dtype=torch.bfloat16, device="cuda")
+    m.orthogonalize(x, out[0], clean)
+    m.orthogonalize(x, out[1], poisoned)
+    assert torch.equal(out[0], out[1]) and bool(out.isfinite().all())
+
+
 def test_offsets_past_32_bits(mua):
     """A state of more than 2^31 values: the last matrix's momentum, and a view
     whose matrices lie more than 2^31 values apart."""
