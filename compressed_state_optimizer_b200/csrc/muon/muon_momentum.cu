@@ -8,7 +8,7 @@
 // formed from the unrounded m' in the same pass. Of 6.06 bytes a value (bf16
 // gradients and direction, 8 bits) HBM would take 0.34 ms for 8 x 11008 x 4096;
 // the update takes 0.55 ms, bound by its 36 instructions a value (a fifth of
-// them Philox, the rest the conversions, the clamp and the packing) at 2.3
+// them Philox, the rest the conversions, the clamp and the packing) at 2.4
 // instructions a cycle; packed fp32 pairs and the next run's loads in flight
 // brought it there from 0.96 ms. Reading back runs at HBM's rate (0.17 ms).
 #include "muon_quant.cuh"
