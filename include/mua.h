@@ -265,7 +265,7 @@ int mua_get_status(mua_t h, const void* state, void* stream, int32_t* out);
  * below 2^-100 is stored as zeros.
  *
  * Precision of X: fp16 operands, fp32 sums; about 1e-3 relative to exact
- * arithmetic in the Frobenius norm, 0.5e-3 for matrices that fit one SM, up to
+ * arithmetic in the Frobenius norm, 0.5e-3 for matrices that fit one SM, some
  * 2.5e-3 for longer ones whose singular values lie close together.
  *
  * The conventions at the top of this header hold. Calls of one handle may run
