@@ -281,8 +281,8 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
   h->lds = row_stride(s);
   h->bpm = bpm;
   h->off_scales = 256;
-  h->off_codes = h->off_scales + round_up(4 * count * bpm, 256);
-  h->state_bytes = h->off_codes + count * bpm * mua::kMuonBlock * bits / 8;
+  h->off_codes = h->off_scales + round_up(4ll * count * bpm, 256);
+  h->state_bytes = h->off_codes + (int64_t)count * bpm * mua::kMuonBlock * bits / 8;
   const int64_t x_bytes = (int64_t)rows * h->ld * 2, a_bytes = (int64_t)s * h->lds * 2;
   const int64_t items = 16 * (((int64_t)s + 127) / 128 * (((int64_t)s + 127) / 128 + 1) * 17 +
                               (((int64_t)rows + 127) / 128) * (((int64_t)cols + 127) / 128));
