@@ -36,6 +36,7 @@ namespace {
 constexpr int kWorkers = 512;             // warps 0 .. 15; warp 16 issues the MMAs
 constexpr int kThreads = kWorkers + 32;
 constexpr uint32_t kOverread = 16384;  // 128 rows of a chunk that starts at its last row
+constexpr uint32_t kMaxSmem = 230000;  // dynamic: 227 KB less what is static
 
 __host__ __device__ __forceinline__ int round16(int x) { return (x + 15) & ~15; }
 
@@ -553,8 +554,10 @@ cudaError_t run(const MuonShape& s, const MuonNs& g, const MuonView& x, const Mu
                 int e0, cudaStream_t st) {
   auto kernel = small_kernel<SRC>;
   const uint32_t smem = muon_small_smem(s.rows, s.cols);
+  // One attribute for all handles of the process: always the same value, so that no
+  // thread's call lowers it before another's launch.
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)s.count, kThreads, smem, st>>>(s, g, x, q, grads, beta, nesterov, rnd, eps, e0);
   return cudaGetLastError();
@@ -565,7 +568,7 @@ cudaError_t run(const MuonShape& s, const MuonNs& g, const MuonView& x, const Mu
 uint32_t muon_small_smem(int32_t rows, int32_t cols) {
   if (std::min(rows, cols) > 128 || std::max(rows, cols) > 8192) return 0;
   const uint32_t bytes = plan_of(rows, cols).bytes + 1024;  // + alignment
-  return bytes <= 230000 ? bytes : 0;
+  return bytes <= kMaxSmem ? bytes : 0;
 }
 
 cudaError_t muon_launch_small(const MuonShape& s, const MuonNs& g, const MuonView& x, float eps,
