@@ -39,6 +39,7 @@
 // MUA_STATUS_TIMEOUT, the CTA's roles stop, copies and MMAs in flight are
 // awaited (bounded again), TMEM is freed and the kernel returns.
 #include <algorithm>
+#include <atomic>
 
 #include "muon_tc.cuh"
 
@@ -715,7 +716,9 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 cudaError_t encode_fn(EncodeFn* out) {
-  static EncodeFn fn = nullptr;  // a process-wide driver entry point
+  // A process-wide driver entry point; threads that ask at once store the same one.
+  static std::atomic<EncodeFn> known{nullptr};
+  EncodeFn fn = known.load(std::memory_order_relaxed);
   if (!fn) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -724,6 +727,7 @@ cudaError_t encode_fn(EncodeFn* out) {
     if (e != cudaSuccess) return e;
     if (found != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
     fn = reinterpret_cast<EncodeFn>(p);
+    known.store(fn, std::memory_order_relaxed);
   }
   *out = fn;
   return cudaSuccess;
@@ -756,14 +760,12 @@ constexpr int kMaxDevices = 64;
 // CTAs of a cooperative launch that the current device holds at once.
 template <int CG, int BN>
 cudaError_t resident_ctas(int* out) {
-  static int known[kMaxDevices];  // 0: not asked yet
+  static std::atomic<int> known[kMaxDevices];  // 0: not asked yet
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < kMaxDevices && known[dev] > 0) {
-    *out = known[dev];
+  if (dev < kMaxDevices && (*out = known[dev].load(std::memory_order_acquire)) > 0)
     return cudaSuccess;
-  }
   auto kernel = ns_kernel<CG, BN>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<BN>::smem);
   if (e != cudaSuccess) return e;
@@ -789,7 +791,7 @@ cudaError_t resident_ctas(int* out) {
   }
   if (e != cudaSuccess) return e;
   if (n < CG) return cudaErrorLaunchOutOfResources;
-  if (dev < kMaxDevices) known[dev] = n;
+  if (dev < kMaxDevices) known[dev].store(n, std::memory_order_release);
   *out = n;
   return cudaSuccess;
 }

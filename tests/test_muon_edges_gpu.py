@@ -14,27 +14,25 @@ def mua():
     return pkg
 
 
-def test_threads_with_matrices_of_different_sizes(mua):
-    """Handles of several on-chip sizes, each called from a thread of its own on
-    a stream of its own: every call is accepted and gives what it gives alone."""
+def run_threads(mua, shapes, calls):
+    """Orthogonalisations of each shape from a thread and a stream of its own:
+    every call is accepted and gives what it gives alone."""
     lib = mua.library()
     jobs = []
-    for rows, cols in ((128, 512), (64, 64), (16, 768), (64, 1400), (20, 30)):
+    for rows, cols in shapes:
         m = mua.Muon(rows, cols)
         g = torch.Generator().manual_seed(rows)
         x = torch.randn(1, rows, cols, generator=g).cuda()
-        alone = torch.empty((1, rows, cols), dtype=torch.bfloat16, device="cuda")
-        ws = m.new_workspace()
-        m.orthogonalize(x, alone, ws)
-        jobs.append((m, x, alone, torch.empty_like(alone), ws, torch.cuda.Stream()))
+        out = torch.empty((1, rows, cols), dtype=torch.bfloat16, device="cuda")
+        jobs.append((m, x, out, m.new_workspace(), torch.cuda.Stream()))
     torch.cuda.synchronize()
     refused, start = [], threading.Barrier(len(jobs))
 
-    def work(m, x, _, out, ws, stream):
+    def work(m, x, out, ws, stream):
         args = (m._h, x.data_ptr(), 0, x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
                 out.stride(1), ws.data_ptr(), 1e-7, stream.cuda_stream)
         start.wait()
-        for _ in range(4000):
+        for _ in range(calls):
             rc = lib.mua_muon_orthogonalize(*args)
             if rc != 0:
                 refused.append((m.rows, m.cols, rc))
@@ -46,5 +44,16 @@ def test_threads_with_matrices_of_different_sizes(mua):
         t.join()
     torch.cuda.synchronize()
     assert not refused
-    for m, _, alone, out, ws, _ in jobs:
+    for m, x, out, ws, _ in jobs:
+        alone = torch.empty_like(out)
+        m.orthogonalize(x, alone, ws)
         assert torch.equal(alone, out) and m.status(ws) == 0
+
+
+def test_threads_with_matrices_of_different_sizes(mua):
+    run_threads(mua, [(128, 512), (64, 64), (16, 768), (64, 1400), (20, 30)], 4000)
+
+
+def test_threads_with_larger_matrices(mua):
+    """The products' launches from several threads, their first ones at once."""
+    run_threads(mua, [(300, 200), (200, 300), (700, 520), (1500, 1600)], 100)
