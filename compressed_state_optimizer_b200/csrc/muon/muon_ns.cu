@@ -539,6 +539,7 @@ ns_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MuonNs g) {
           ready = it.before;
         }
         reduce_rows<CG, BN>(g, walk.T, it, rank, warp - 2, lane, alpha);
+        __syncwarp();  // the lanes' rows before the arrival that counts them
         // No warp arrives for an item before all have arrived for the last one.
         ok = mbar_wait_warp(smem_u32(&room), (out_items & 1u) ^ 1u, g.wait_ns, stop_v);
         if (!ok) break;

@@ -57,3 +57,22 @@ def test_threads_with_matrices_of_different_sizes(mua):
 def test_threads_with_larger_matrices(mua):
     """The products' launches from several threads, their first ones at once."""
     run_threads(mua, [(300, 200), (200, 300), (700, 520), (1500, 1600)], 100)
+
+
+@pytest.mark.parametrize("count,rows,cols", [(1, 200, 8000), (2, 5000, 129), (1, 512, 11008)])
+def test_shared_contractions_repeat(mua, count, rows, cols):
+    """Where several CTAs share a tile's contraction, what is added up reaches
+    the product that reads it: the same bytes on each of many runs."""
+    m = mua.Muon(rows, cols, count)
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn(count, rows, cols, generator=g).cuda()
+    ws, other = m.new_workspace(), m.new_workspace()
+    first = torch.empty((count, rows, cols), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(first)
+    m.orthogonalize(x, first, ws)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for k in range(60):
+        other[256:] = k  # nothing of an earlier run is left
+        m.orthogonalize(x, out, other)
+        differ += (out != first).sum()
+    assert int(differ) == 0 and bool(first.isfinite().all()) and m.status(other) == 0
