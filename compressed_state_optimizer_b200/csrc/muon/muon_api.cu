@@ -326,6 +326,11 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
+// All values of a handle's stack, contiguous.
+int64_t value_bytes(const mua_muon_ctx* h, int32_t type) {
+  return (int64_t)h->rows * h->cols * h->count * type_size(type);
+}
+
 }  // namespace
 
 extern "C" {
@@ -366,8 +371,9 @@ int mua_muon_momentum(mua_muon_t h, const void* grads, int32_t grads_type, void*
   if (!aligned(grads, type_size(grads_type)) || !aligned(direction, type_size(direction_type)) ||
       !aligned(state, 16))
     return MUA_ERR_ALIGN;
-  const int64_t n = (int64_t)h->rows * h->cols * h->count;
-  if (overlap(grads, n * type_size(grads_type), direction, n * type_size(direction_type)))
+  const int64_t gs = value_bytes(h, grads_type), ds = value_bytes(h, direction_type);
+  if (overlap(grads, gs, direction, ds) || overlap(grads, gs, state, h->state_bytes) ||
+      overlap(direction, ds, state, h->state_bytes))
     return MUA_ERR_ARG;
   const cudaError_t e = mua::muon_launch_momentum(
       shape(h, h->count), quant(h, state, 0), grads, grads_type, beta, nesterov != 0,
@@ -379,6 +385,7 @@ int mua_muon_momentum(mua_muon_t h, const void* grads, int32_t grads_type, void*
 int mua_muon_read(mua_muon_t h, const void* state, void* out, int32_t type, void* stream) {
   if (!h || !state || !out || !valid_type(type)) return MUA_ERR_ARG;
   if (!aligned(state, 16) || !aligned(out, type_size(type))) return MUA_ERR_ALIGN;
+  if (overlap(out, value_bytes(h, type), state, h->state_bytes)) return MUA_ERR_ARG;
   const cudaError_t e = mua::muon_launch_read(shape(h, h->count), quant(h, state, 0), out, type,
                                               static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MUA_OK : fail(e, "read kernel launch");
@@ -387,6 +394,7 @@ int mua_muon_read(mua_muon_t h, const void* state, void* out, int32_t type, void
 int mua_muon_write(mua_muon_t h, const void* values, int32_t type, void* state, void* stream) {
   if (!h || !state || !values || !valid_type(type)) return MUA_ERR_ARG;
   if (!aligned(state, 16) || !aligned(values, type_size(type))) return MUA_ERR_ALIGN;
+  if (overlap(values, value_bytes(h, type), state, h->state_bytes)) return MUA_ERR_ARG;
   const cudaError_t e = mua::muon_launch_write(shape(h, h->count), quant(h, state, 0), values, type,
                                                static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MUA_OK : fail(e, "write kernel launch");
@@ -412,6 +420,9 @@ int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t 
   const int64_t x_span = last * x_matrix_stride + (h->rows - 1) * x_row_stride + row;
   const int64_t out_span = last * out_matrix_stride + (h->rows - 1) * out_row_stride + row;
   if (!same && overlap(x, x_span * type_size(x_type), out, out_span * 2)) return MUA_ERR_ARG;
+  if (overlap(x, x_span * type_size(x_type), workspace, h->workspace_bytes) ||
+      overlap(out, out_span * 2, workspace, h->workspace_bytes))
+    return MUA_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   double* partials = reinterpret_cast<double*>(ws + h->off_partials);
@@ -452,9 +463,11 @@ int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* g
   if (!aligned(params, type_size(params_type)) || !aligned(grads, type_size(grads_type)) ||
       !aligned(state, 16) || !aligned(workspace, 16))
     return MUA_ERR_ALIGN;
-  const int64_t all = (int64_t)h->rows * h->cols * h->count;
-  if (overlap(params, all * type_size(params_type), grads, all * type_size(grads_type)) ||
-      overlap(state, h->state_bytes, workspace, h->workspace_bytes))
+  const int64_t ps = value_bytes(h, params_type), gs = value_bytes(h, grads_type);
+  if (overlap(params, ps, grads, gs) || overlap(state, h->state_bytes, workspace, h->workspace_bytes) ||
+      overlap(params, ps, state, h->state_bytes) || overlap(grads, gs, state, h->state_bytes) ||
+      overlap(params, ps, workspace, h->workspace_bytes) ||
+      overlap(grads, gs, workspace, h->workspace_bytes))
     return MUA_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);

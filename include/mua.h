@@ -325,7 +325,8 @@ int mua_muon_state_layout(mua_muon_t h, int64_t* out);
 /*
  * mua_muon_momentum - the momentum update alone: grads (count x rows x cols of
  * grads_type, contiguous) into the state, and the direction U (contiguous, of
- * direction_type) out. grads and direction must not overlap (MUA_ERR_ARG).
+ * direction_type) out. grads, state and direction must not overlap
+ * (MUA_ERR_ARG).
  */
 int mua_muon_momentum(mua_muon_t h, const void* grads, int32_t grads_type, void* state,
                       void* direction, int32_t direction_type, float beta, int32_t nesterov,
@@ -334,7 +335,8 @@ int mua_muon_momentum(mua_muon_t h, const void* grads, int32_t grads_type, void*
 /*
  * mua_muon_read / mua_muon_write - the momentum as contiguous values, and back
  * (each value to its block's nearest level, ties to even: what was read as
- * fp32 is written as the same codes).
+ * fp32 is written as the same codes). The values and the state must not
+ * overlap (MUA_ERR_ARG).
  */
 int mua_muon_read(mua_muon_t h, const void* state, void* out, int32_t type, void* stream);
 int mua_muon_write(mua_muon_t h, const void* values, int32_t type, void* state, void* stream);
@@ -343,9 +345,9 @@ int mua_muon_write(mua_muon_t h, const void* values, int32_t type, void* state, 
  * mua_muon_orthogonalize - X_steps of a stack of matrices x, to the bf16 stack
  * out. Strides count elements; columns are contiguous. x may be broadcast
  * (stride 0); the rows of out must not overlap. out may be x itself (bf16, the
- * same strides); otherwise the two address ranges must not overlap
- * (MUA_ERR_ARG). eps >= 0. A matrix of zeros gives zeros; one with a NaN or
- * infinity gives NaN.
+ * same strides); otherwise the two address ranges must not overlap, nor may
+ * either with the workspace (MUA_ERR_ARG). eps >= 0. A matrix of zeros gives
+ * zeros; one with a NaN or infinity gives NaN.
  */
 int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t x_matrix_stride,
                            int64_t x_row_stride, void* out, int64_t out_matrix_stride,
@@ -354,7 +356,7 @@ int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t 
 /*
  * mua_muon_step - the whole step t (1, 2, ...) on `stream`: params (fp32 or
  * bf16, contiguous) are updated in place, formed in fp32 and rounded once.
- * X_steps is not rounded to bf16 on the way. params and grads, state and
+ * X_steps is not rounded to bf16 on the way. params, grads, state and
  * workspace must not overlap (MUA_ERR_ARG).
  */
 int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* grads,
