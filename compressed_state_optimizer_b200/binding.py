@@ -408,7 +408,8 @@ class Muon:
                      (state.data_ptr(), out.data_ptr(), ot))
 
     def write_momentum(self, values, state, stream=None):
-        """``values`` (fp32 or bf16) as the momentum, each to the nearest level."""
+        """``values`` (fp32 or bf16) as the momentum, each to the nearest level of
+        its block. A copy of the state, not its values, is the exact checkpoint."""
         vt = self._values(values, "values")
         self._buffer(state, self.state_bytes, "state")
         self._launch("mua_muon_write", stream, (values, state),

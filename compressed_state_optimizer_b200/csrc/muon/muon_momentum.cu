@@ -282,8 +282,8 @@ read_kernel(MuonShape s, MuonQuant Q, void* out, int splits) {
   }
 }
 
-// Codes of given values, each to the nearest level (ties to even): values
-// read from a state come back as the same codes.
+// Codes of given values, each to the nearest level (ties to even). Values read
+// from a block that holds level L come back as the same codes.
 template <int BITS, int T>
 __global__ void __launch_bounds__(kThreads)
 write_kernel(MuonShape s, MuonQuant Q, const void* values, int splits) {

@@ -334,9 +334,12 @@ int mua_muon_momentum(mua_muon_t h, const void* grads, int32_t grads_type, void*
 
 /*
  * mua_muon_read / mua_muon_write - the momentum as contiguous values, and back
- * (each value to its block's nearest level, ties to even: what was read as
- * fp32 is written as the same codes). The values and the state must not
- * overlap (MUA_ERR_ARG).
+ * (each value to its block's nearest level, ties to even). They carry values:
+ * a block whose largest code is L comes back with the same codes and a scale
+ * that may differ in its last places; one that an update left without level L
+ * (a draw of 0 can store L - 1 for the largest value) is rounded anew, each
+ * value within half a level. What repeats a run bit for bit is a copy of the
+ * state's bytes. The values and the state must not overlap (MUA_ERR_ARG).
  */
 int mua_muon_read(mua_muon_t h, const void* state, void* out, int32_t type, void* stream);
 int mua_muon_write(mua_muon_t h, const void* values, int32_t type, void* state, void* stream);

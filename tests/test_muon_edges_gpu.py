@@ -1,8 +1,12 @@
 """The Muon entry points at the edges, on a GPU."""
 import threading
 
+import numpy as np
 import pytest
 import torch
+
+import muon_ref
+from muon_ref import U32
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +80,45 @@ def test_shared_contractions_repeat(mua, count, rows, cols):
         m.orthogonalize(x, out, other)
         differ += (out != first).sum()
     assert int(differ) == 0 and bool(first.isfinite().all()) and m.status(other) == 0
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_states_that_updates_left_are_read_and_written(mua, bits):
+    """Blocks with level L come back with their codes; one whose largest level is
+    below L, as an update can leave it, with values within half a level. A copy
+    of the bytes goes on as the state itself does."""
+    count, rows, cols = 3, 77, 530
+    n, level = rows * cols, 2 ** (bits - 1) - 1
+    m = mua.Muon(rows, cols, count, bits=bits)
+    st = m.new_state()
+    u = torch.empty(m.d, device="cuda")
+    gen = torch.Generator().manual_seed(bits)
+    grads = [torch.randn(m.d, generator=gen).cuda() for _ in range(4)]
+    for t in range(3):
+        m.momentum(grads[t], st, u, beta=0.95, t=t + 1, seed=21)
+    # As a draw of 0 leaves it: every level L of every fifth block one lower.
+    q, _ = muon_ref.unpack(st.cpu().numpy(), m.layout, count, n, bits)
+    q[::5] = np.clip(q[::5], 1 - level, level - 1)
+    raw = q.astype(np.int8).view(np.uint8).reshape(-1)
+    raw = raw if bits == 8 else (raw[0::2] & 15) | (raw[1::2] << 4)
+    st[m.layout.codes:] = torch.from_numpy(raw).cuda()
+
+    values, again = torch.empty(m.d, device="cuda"), torch.empty(m.d, device="cuda")
+    written, copied = m.new_state(), st.clone()
+    m.read_momentum(st, values)
+    m.write_momentum(values, written)
+    m.read_momentum(written, again)
+    q1, s1 = muon_ref.unpack(st.cpu().numpy(), m.layout, count, n, bits)
+    q2, s2 = muon_ref.unpack(written.cpu().numpy(), m.layout, count, n, bits)
+    full = np.abs(q1).max(1) == level
+    assert 0.7 < full.mean() < 0.9
+    assert np.array_equal(q1[full], q2[full])
+    assert (np.abs(s1 - s2)[full] <= 4 * U32 * s1[full]).all()
+    # half a level, and four roundings of values of up to L levels
+    v = muon_ref.blocks_of(values.cpu().numpy().astype(np.float64).reshape(count, n))
+    w = muon_ref.blocks_of(again.cpu().numpy().astype(np.float64).reshape(count, n))
+    assert (np.abs(v - w) <= s2[:, None].astype(np.float64) * (0.5 + 4 * U32 * level)).all()
+    other = torch.empty_like(u)
+    m.momentum(grads[3], st, u, beta=0.95, t=4, seed=21)
+    m.momentum(grads[3], copied, other, beta=0.95, t=4, seed=21)
+    assert torch.equal(st, copied) and torch.equal(u, other)
