@@ -48,19 +48,27 @@ __device__ __forceinline__ uint64_t f2_fma_rm(uint64_t a, uint64_t b, uint64_t c
 }
 
 // Eight consecutive values of type T from p[i ..], those at or past n as 0.
-template <int T>
+// CONSTANT: nothing in the launch writes them, so that the read-only path is open.
+template <int T, bool CONSTANT = true>
 __device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, bool vec,
                                       uint64_t (&v)[4]) {
+  auto load = [](const void* at) {
+    if constexpr (CONSTANT) return ld_stream_v4(at);
+    uint4 w;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(at) : "memory");
+    return w;
+  };
   if (vec && i + 8 <= n) {
     if constexpr (T == kBf16) {
-      const uint4 w = ld_stream_v4(static_cast<const uint16_t*>(p) + i);
+      const uint4 w = load(static_cast<const uint16_t*>(p) + i);
       v[0] = f2_pack(bf16_lo(w.x), bf16_hi(w.x));
       v[1] = f2_pack(bf16_lo(w.y), bf16_hi(w.y));
       v[2] = f2_pack(bf16_lo(w.z), bf16_hi(w.z));
       v[3] = f2_pack(bf16_lo(w.w), bf16_hi(w.w));
     } else {
       const float* f = static_cast<const float*>(p) + i;
-      const uint4 a = ld_stream_v4(f), b = ld_stream_v4(f + 4);
+      const uint4 a = load(f), b = load(f + 4);
       v[0] = f2_pack(__uint_as_float(a.x), __uint_as_float(a.y));
       v[1] = f2_pack(__uint_as_float(a.z), __uint_as_float(a.w));
       v[2] = f2_pack(__uint_as_float(b.x), __uint_as_float(b.y));

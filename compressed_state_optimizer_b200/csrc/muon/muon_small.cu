@@ -206,7 +206,8 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
     for (uint32_t o = threadIdx.x * 16; worker && o < p.hi_off; o += kWorkers * 16)
       st_shared(X + o, 0u, 0u, 0u, 0u);
 
-  // The norm, then X_0 = x 2^(e0 - t): see muon_launch_load.
+  // The norm, then X_0 = x 2^(e0 - t): see muon_launch_load. bf16 matrices may be
+  // the result's own memory.
   if constexpr (!STEP) {
     const int es = T == kBf16 ? 2 : 4;
     const uint8_t* xm = static_cast<const uint8_t*>(x.p) + mat * x.matrix_stride * es;
@@ -230,7 +231,8 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
         const uint32_t q = q0 + k * kWorkers;
         int row, col;
         place(q, row, col);
-        load8<T>(xm + (int64_t)row * x.row_stride * es, col, q < groups ? sh.cols : 0, vec, held[k]);
+        load8<T, T != kBf16>(xm + (int64_t)row * x.row_stride * es, col, q < groups ? sh.cols : 0, vec,
+                             held[k]);
       }
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) sum += sum_squares(held[k]);
@@ -245,7 +247,7 @@ small_kernel(MuonShape sh, const __grid_constant__ MuonNs g, MuonView x, MuonQua
       place(q, row, col);
       uint64_t v[4];
       if (groups > kHeld * kWorkers) {
-        load8<T>(xm + (int64_t)row * x.row_stride * es, col, sh.cols, vec, v);
+        load8<T, T != kBf16>(xm + (int64_t)row * x.row_stride * es, col, sh.cols, vec, v);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = k == 0 ? held[0][e] : held[1][e];

@@ -122,3 +122,19 @@ def test_states_that_updates_left_are_read_and_written(mua, bits):
     m.momentum(grads[3], st, u, beta=0.95, t=4, seed=21)
     m.momentum(grads[3], copied, other, beta=0.95, t=4, seed=21)
     assert torch.equal(st, copied) and torch.equal(u, other)
+
+
+@pytest.mark.parametrize("count,rows,cols", [(40, 64, 72), (300, 24, 20), (9, 100, 333),
+                                             (9, 333, 100), (2, 128, 512)])
+def test_in_place_on_one_sm(mua, count, rows, cols):
+    """Matrices side by side in one buffer, woven row by row, each replaced by
+    its result while its neighbours in the same lines of memory are read."""
+    gen = torch.Generator().manual_seed(cols)
+    x = torch.randn(count, rows, cols, generator=gen).to(torch.bfloat16).cuda()
+    m = mua.Muon(rows, cols, count)
+    ws = m.new_workspace()
+    want = torch.empty_like(x)
+    m.orthogonalize(x, want, ws)
+    for lay in (x.clone(), x.transpose(0, 1).contiguous().transpose(0, 1)):
+        m.orthogonalize(lay, lay, ws)
+        assert torch.equal(lay, want)
