@@ -138,8 +138,8 @@ uint32_t* counters(const mua_muon_ctx* h, uint8_t* ws) {
 }
 
 // The iteration of matrices first .. first + count - 1.
-mua::MuonNs iteration(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count,
-                      const Target& to, uint32_t* status) {
+mua::MuonNs iteration(const mua_muon_ctx* h, int32_t first, int32_t count, const Target& to,
+                      uint32_t* status) {
   mua::MuonNs g;
   std::memset(&g, 0, sizeof g);
   g.rows = h->rows;
@@ -157,7 +157,6 @@ mua::MuonNs iteration(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t
                                      : std::ldexp(1.0, h->ex[k + 1] - ep - ex));
   }
   const int64_t size = type_size(to.type);
-  g.factor = reinterpret_cast<const float*>(ws + h->off_factor);
   g.out = static_cast<uint8_t*>(to.out) + (int64_t)first * to.matrix_stride * size;
   g.ldo = to.row_stride;
   g.batch_stride = to.matrix_stride;
@@ -167,7 +166,6 @@ mua::MuonNs iteration(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t
   g.out_vec = aligned(g.out, 4 * size) && to.row_stride % 4 == 0 &&
               (count == 1 || to.matrix_stride % 4 == 0);
   g.decay = to.decay;
-  g.counters = counters(h, ws);
   g.status = status;
   g.wait_ns = (uint64_t)std::max<int64_t>(0, h->wait_ns);
   return g;
@@ -176,7 +174,9 @@ mua::MuonNs iteration(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t
 // Its launch, X_0 and its factors being in the workspace.
 int iterate(const mua_muon_ctx* h, uint8_t* ws, int32_t first, int32_t count, const Target& to,
             uint32_t* status, cudaStream_t st) {
-  mua::MuonNs g = iteration(h, ws, first, count, to, status);
+  mua::MuonNs g = iteration(h, first, count, to, status);
+  g.factor = reinterpret_cast<const float*>(ws + h->off_factor);
+  g.counters = counters(h, ws);
   g.x[0] = ws + h->off_x[0];
   g.x[1] = ws + h->off_x[1];
   g.a = ws + h->off_a;
@@ -283,6 +283,12 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
   h->off_scales = 256;
   h->off_codes = h->off_scales + round_up(4ll * count * bpm, 256);
   h->state_bytes = h->off_codes + (int64_t)count * bpm * mua::kMuonBlock * bits / 8;
+  h->wait_ns = kDefaultWaitNs;
+  h->workspace_bytes = 256;  // the status word
+  if (h->small) {  // nothing of such a matrix leaves its SM
+    *out = h;
+    return MUA_OK;
+  }
   const int64_t x_bytes = (int64_t)rows * h->ld * 2, a_bytes = (int64_t)s * h->lds * 2;
   const int64_t items = 16 * (((int64_t)s + 127) / 128 * (((int64_t)s + 127) / 128 + 1) * 17 +
                               (((int64_t)rows + 127) / 128) * (((int64_t)cols + 127) / 128));
@@ -295,7 +301,7 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
   // The norm's sums: four CTAs an SM of a B200 in all, 8192 values each or more.
   h->parts = (int32_t)std::max<int64_t>(
       1, std::min<int64_t>(4 * 148 / h->group, n / 8192));
-  int64_t at = 256;
+  int64_t at = h->workspace_bytes;
   auto take = [&at](int64_t bytes) {
     const int64_t o = at;
     at += round_up(bytes, 256);
@@ -314,7 +320,6 @@ int create(int32_t rows, int32_t cols, int32_t count, int32_t bits, int32_t step
                             h->tiling.bn * h->tiling.bn)
                      : at;
   h->workspace_bytes = at;
-  h->wait_ns = kDefaultWaitNs;
   *out = h;
   return MUA_OK;
 }
@@ -425,16 +430,16 @@ int mua_muon_orthogonalize(mua_muon_t h, const void* x, int32_t x_type, int64_t 
     return MUA_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  double* partials = reinterpret_cast<double*>(ws + h->off_partials);
   const Target to = {false, out, MUA_BF16, out_matrix_stride, out_row_stride, 1.0, 0.0f};
   uint32_t* status = reinterpret_cast<uint32_t*>(ws) + mua::kMuonHdrStatus;
   if (h->small) {
     const mua::MuonView v = {const_cast<void*>(x), x_type, x_matrix_stride, x_row_stride};
     const cudaError_t e =
-        mua::muon_launch_small(shape(h, h->count), iteration(h, ws, 0, h->count, to, status), v,
+        mua::muon_launch_small(shape(h, h->count), iteration(h, 0, h->count, to, status), v,
                                eps, h->ex[0], st);
     return e == cudaSuccess ? MUA_OK : fail(e, "orthogonalization kernel launch");
   }
+  double* partials = reinterpret_cast<double*>(ws + h->off_partials);
   for (int32_t first = 0; first < h->count; first += h->group) {
     const int32_t count = std::min(h->group, h->count - first);
     const mua::MuonView v = {
@@ -471,18 +476,18 @@ int mua_muon_step(mua_muon_t h, void* params, int32_t params_type, const void* g
     return MUA_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  double* partials = reinterpret_cast<double*>(ws + h->off_partials);
-  float* factor = reinterpret_cast<float*>(ws + h->off_factor);
   const int64_t n = (int64_t)h->rows * h->cols;
   const Target to = {true, params, params_type, n, h->cols,
                      (double)lr * (double)scale, (float)(1.0 - (double)lr * (double)wd)};
   uint32_t* status = static_cast<uint32_t*>(state) + mua::kMuonHdrStatus;
   if (h->small) {
     const cudaError_t e = mua::muon_launch_small_step(
-        shape(h, h->count), iteration(h, ws, 0, h->count, to, status), quant(h, state, 0), grads,
+        shape(h, h->count), iteration(h, 0, h->count, to, status), quant(h, state, 0), grads,
         grads_type, beta, nesterov != 0, random_keys(h, 0, t, seed), eps, h->ex[0], st);
     return e == cudaSuccess ? MUA_OK : fail(e, "step kernel launch");
   }
+  double* partials = reinterpret_cast<double*>(ws + h->off_partials);
+  float* factor = reinterpret_cast<float*>(ws + h->off_factor);
   for (int32_t first = 0; first < h->count; first += h->group) {
     const int32_t count = std::min(h->group, h->count - first);
     const mua::MuonShape s = shape(h, count);

@@ -86,3 +86,17 @@ def test_values_over_a_state_or_a_workspace_are_refused(mua, call):
 def test_neighbouring_buffers_are_accepted(mua, call):
     """They pass the host checks; the launch then finds no GPU."""
     refused_without_a_gpu(mua, call, -4)
+
+
+@pytest.mark.parametrize("rows,cols,count", [(64, 64, 10000), (1, 1, 1 << 30), (16, 768, 1),
+                                             (128, 512, 48), (5000, 16, 3), (20, 30, 1)])
+def test_matrices_on_one_sm_need_no_scratch(mua, rows, cols, count):
+    """Their workspace is its status word's 256 bytes."""
+    assert mua.Muon(rows, cols, count).workspace_bytes == 256
+
+
+@pytest.mark.parametrize("rows,cols,count", [(129, 129, 1), (16, 9000, 2), (128, 600, 1)])
+def test_other_matrices_have_theirs(mua, rows, cols, count):
+    """X twice, A and P in 2 bytes a value."""
+    s = min(rows, cols)
+    assert mua.Muon(rows, cols, count).workspace_bytes >= 256 + count * (4 * rows * cols + 4 * s * s)
