@@ -568,7 +568,7 @@ cudaError_t run(const MuonShape& s, const MuonNs& g, const MuonView& x, const Mu
 }  // namespace
 
 uint32_t muon_small_smem(int32_t rows, int32_t cols) {
-  if (std::min(rows, cols) > 128 || std::max(rows, cols) > 8192) return 0;
+  if (std::min(rows, cols) > 128) return 0;
   const uint32_t bytes = plan_of(rows, cols).bytes + 1024;  // + alignment
   return bytes <= kMaxSmem ? bytes : 0;
 }

@@ -100,3 +100,15 @@ def test_other_matrices_have_theirs(mua, rows, cols, count):
     """X twice, A and P in 2 bytes a value."""
     s = min(rows, cols)
     assert mua.Muon(rows, cols, count).workspace_bytes >= 256 + count * (4 * rows * cols + 4 * s * s)
+
+
+@pytest.mark.parametrize("short,longest", [(1, 6464), (16, 6464), (32, 3136), (48, 2048), (64, 1472),
+                                           (80, 1024), (96, 832), (112, 640), (128, 512)])
+def test_what_fits_one_sm(mua, short, longest):
+    """The longest matrix of a shorter side that stays on one SM, either way up:
+    its three matrices' tiles, and what an MMA reads behind the last, in 230000
+    bytes."""
+    on_chip = lambda r, c: mua.Muon(r, c).workspace_bytes == 256  # noqa: E731
+    for far in (longest + 1, 1 << 13, 1 << 16, 1 << 20):
+        assert not on_chip(short, far) and not on_chip(far, short)
+    assert on_chip(short, longest) and on_chip(longest, short)
