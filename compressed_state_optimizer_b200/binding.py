@@ -295,6 +295,10 @@ class Muon:
     def __init__(self, rows: int, cols: int, count: int = 1, *, bits: int = 8, steps: int = 5,
                  coefficients=None):
         lib = library()
+        for name, v in (("rows", rows), ("cols", cols), ("count", count), ("bits", bits),
+                        ("steps", steps)):
+            if not -(1 << 31) <= v < 1 << 31:  # ctypes would pass its low half
+                raise ValueError(f"{name}: {v} does not fit 32 bits")
         arr = None
         if coefficients is not None:
             c = list(coefficients)

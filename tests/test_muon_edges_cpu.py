@@ -112,3 +112,17 @@ def test_what_fits_one_sm(mua, short, longest):
     for far in (longest + 1, 1 << 13, 1 << 16, 1 << 20):
         assert not on_chip(short, far) and not on_chip(far, short)
     assert on_chip(short, longest) and on_chip(longest, short)
+
+
+@pytest.mark.parametrize("args", [((1 << 32) + 4, 4, 1), (4, (1 << 32) + 4, 1), (4, 4, (1 << 32) + 1),
+                                  (1 << 31, 1, 1), (4, 4, 1 << 31), (-(1 << 32) + 4, 4, 1)])
+def test_sizes_past_32_bits_are_refused(mua, args):
+    """They do not become the smaller sizes that their low halves are."""
+    with pytest.raises(ValueError):
+        mua.Muon(*args)
+
+
+@pytest.mark.parametrize("kw", [dict(bits=(1 << 32) + 8), dict(steps=(1 << 32) + 5)])
+def test_options_past_32_bits_are_refused(mua, kw):
+    with pytest.raises(ValueError):
+        mua.Muon(4, 4, **kw)
