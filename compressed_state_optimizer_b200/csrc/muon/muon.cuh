@@ -14,9 +14,10 @@
 // norm is summed in fp32 or fp64. Against fp64, simulated for a Gaussian matrix
 // of 768 x 768: 1.2e-3 relative in the Frobenius norm (bf16 operands: 1.0e-2;
 // the final rounding to bf16 alone: 1.7e-3). Matrices that stay on one SM hold A
-// and P as two fp16 values each: 0.5e-3. Where the singular values lie close
-// together, as of a long Gaussian matrix of few rows, the diagonals of A and P
-// round alike and the errors add up: 2.2e-3 for 26 x 8319.
+// and P as two fp16 values each: 0.5e-3 for long ones, 0.8e-3 to 1e-3 for square
+// ones. Where the singular values lie close together, as of a long Gaussian matrix
+// of few rows, the diagonals of A and P round alike and the errors add up: 2.2e-3
+// for 26 x 8319.
 #pragma once
 
 #include <cstdint>

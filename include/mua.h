@@ -264,9 +264,13 @@ int mua_get_status(mua_t h, const void* state, void* stream, int32_t* out);
  * number * 128 + position, t, seed): unbiased. A block whose largest value is
  * below 2^-100 is stored as zeros.
  *
- * Precision of X: fp16 operands, fp32 sums; about 1e-3 relative to exact
- * arithmetic in the Frobenius norm, 0.5e-3 for matrices that fit one SM, some
- * 2.5e-3 for longer ones whose singular values lie close together.
+ * Precision of X: fp16 operands, fp32 sums. Relative to exact arithmetic in the
+ * Frobenius norm 1e-3 to 1.3e-3, and up to 2.6e-3 for long matrices of few rows,
+ * whose singular values lie close together. Matrices that fit one SM: 0.5e-3
+ * where one side is several times the other, 0.8e-3 to 1e-3 for square ones, up
+ * to 2e-3 where a side is below 16 and few roundings average out. A norm far
+ * below eps leaves X_0 an absolute precision of 2^-38 an entry; |U|_F + eps below
+ * 2^-126 counts as zero.
  *
  * The conventions at the top of this header hold. Calls of one handle may run
  * at once when they use different states and workspaces; a workspace belongs

@@ -134,3 +134,39 @@ def test_small_values_decay_beside_a_steady_one(mua, bits, start):
     # six deviations of the mean of 64 * 127 values
     room = 6 * math.sqrt(0.25 / (1 - 0.95 ** 2)) / math.sqrt(64 * 127)
     assert abs(float(got[:, 1:].mean()) - start * 0.95 ** 60) <= room
+
+
+@pytest.mark.parametrize("count,rows,cols", [(2, 64, 300), (1, 300, 520)])
+def test_matrices_of_tiny_values(mua, count, rows, cols):
+    """eps = 0: values down to the smallest of their type keep the precision of
+    ordinary ones; a norm below 2^-126 gives zeros."""
+    host = muon_formats.matrices("normal", count, rows, cols) * np.float32(2.0 ** -127)
+    assert (np.abs(host) < 2.0 ** -126).mean() > 0.9   # most are subnormal
+    m = mua.Muon(rows, cols, count)
+    ws = m.new_workspace()
+    out = torch.empty((count, rows, cols), dtype=torch.bfloat16, device="cuda")
+    m.orthogonalize(torch.from_numpy(host).cuda(), out, ws, eps=0.0)
+    for k, a in enumerate(host.astype(np.float64)):
+        want = muon_ref.orthogonalize(a, eps=0.0)
+        allowed = ROOM * error(muon_formats.iterate(a, m.workspace_bytes == 256, eps=0.0), want)
+        assert error(out[k].double().cpu().numpy(), want) <= allowed + UBF
+    m.orthogonalize(torch.from_numpy(host * np.float32(2.0 ** -9)).cuda(), out, ws, eps=0.0)
+    assert torch.count_nonzero(out) == 0 and m.status(ws) == 0
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 300), (300, 520)])
+def test_norms_far_below_eps(mua, rows, cols):
+    """X_0 keeps an absolute precision then: an entry is off by 2^-38 at most, and
+    the iteration multiplies it by 3.4445 a step."""
+    host = muon_formats.matrices("normal", 1, rows, cols)[0]
+    m = mua.Muon(rows, cols)
+    for below in (2.0 ** -10, 2.0 ** -25, 2.0 ** -60):
+        eps = float(np.float32(np.linalg.norm(host) / below))
+        got = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+        m.orthogonalize(torch.from_numpy(host).cuda(), got, m.new_workspace(), eps=eps)
+        want = muon_ref.orthogonalize(host.astype(np.float64), eps=eps)
+        off = np.linalg.norm(got.double().cpu().numpy() - want)
+        # half a step of fp16 from each of the five X and P; below its normal range
+        # each X adds 2^-39 an entry (X_0 twice that), grown through the steps left
+        grown = 3.4445 ** 5 * (2.0 ** -39) * 5 * math.sqrt(rows * cols)
+        assert off <= (10 * 2.0 ** -11 + UBF) * 1.25 * np.linalg.norm(want) + grown
