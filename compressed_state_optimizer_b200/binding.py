@@ -288,7 +288,8 @@ class Muon:
     The state and the workspace are caller-owned ``torch.uint8`` tensors (see
     :meth:`new_state` and :meth:`new_workspace`). A workspace serves one call
     at a time; calls on several streams, or captured graphs that may overlap,
-    take one each. None of this is differentiable: tensors that would record a
+    take one each. Rounding draws go by (seed, t, place in the stack): give every
+    stack a seed of its own. None of this is differentiable: tensors that would record a
     gradient are refused, except the parameters ``step`` updates in place.
     """
 

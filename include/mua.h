@@ -262,7 +262,10 @@ int mua_get_status(mua_t h, const void* state, void* stream, int32_t* out);
  * 7. The update writes s' = max|m'| / L and q' = floor(m' / s' + r / 2^16), r
  * the value's 16-bit Philox4x32-10 draw as in mua_step (element index: block
  * number * 128 + position, t, seed): unbiased. A block whose largest value is
- * below 2^-100 is stored as zeros.
+ * below 2^-100 is stored as zeros. Every handle counts its blocks from 0: two
+ * stacks that step with the same seed and t round with the same draws, place by
+ * place, and the parts of a stack do not repeat the whole one's bytes. Give each
+ * stack, and each rank's part of one, a seed of its own.
  *
  * Precision of X: fp16 operands, fp32 sums. Relative to exact arithmetic in the
  * Frobenius norm 1e-3 to 1.3e-3, and up to 2.6e-3 for long matrices of few rows,
@@ -278,7 +281,8 @@ int mua_get_status(mua_t h, const void* state, void* stream, int32_t* out);
  * Pointers to values need the alignment of their type, states and workspaces
  * 16 bytes. A NaN or infinity in m', or in a step's U, sets
  * MUA_STATUS_NONFINITE in the state and makes that matrix's results NaN or
- * unspecified; other matrices are not affected. MUA_ERR_CUDA's text is given by mua_muon_last_cuda_error().
+ * unspecified; other matrices are not affected. MUA_ERR_CUDA's text is given by
+ * mua_muon_last_cuda_error().
  */
 #define MUA_F32 0  /* types of values */
 #define MUA_BF16 1

@@ -138,3 +138,22 @@ def test_in_place_on_one_sm(mua, count, rows, cols):
     for lay in (x.clone(), x.transpose(0, 1).contiguous().transpose(0, 1)):
         m.orthogonalize(lay, lay, ws)
         assert torch.equal(lay, want)
+
+
+def test_draws_go_by_seed_and_place(mua):
+    """The same seed rounds two stacks alike, another one does not; a part that
+    starts inside a stack draws from the beginning."""
+    gen = torch.Generator().manual_seed(4)
+    g = torch.randn(2 * 64 * 96, generator=gen).cuda()
+    g[64 * 96:] = g[:64 * 96]
+    whole, part = mua.Muon(64, 96, 2), mua.Muon(64, 96)
+
+    def codes(m, grads, seed):
+        st, u = m.new_state(), torch.empty(m.d, device="cuda")
+        m.momentum(grads, st, u, beta=0.9, t=1, seed=seed)
+        return st[m.layout.codes:].view(m.count, -1)
+
+    both = codes(whole, g, 7)
+    one = codes(part, g[:64 * 96], 7)
+    assert torch.equal(both[0], one[0]) and not torch.equal(both[1], one[0])
+    assert not torch.equal(codes(part, g[:64 * 96], 8)[0], one[0])
