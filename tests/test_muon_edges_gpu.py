@@ -1,4 +1,7 @@
 """The Muon entry points at the edges, on a GPU."""
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -9,6 +12,8 @@ import muon_ref
 from muon_ref import U32
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 @pytest.fixture(scope="module")
 def mua():
@@ -157,3 +162,72 @@ def test_draws_go_by_seed_and_place(mua):
     one = codes(part, g[:64 * 96], 7)
     assert torch.equal(both[0], one[0]) and not torch.equal(both[1], one[0])
     assert not torch.equal(codes(part, g[:64 * 96], 8)[0], one[0])
+
+
+_FIRST_IN_A_CAPTURE = """
+import sys, torch
+sys.path.insert(0, {root!r})
+import compressed_state_optimizer_b200 as mua
+jobs = []
+for rows, cols, bits in ((64, 80, 8), (300, 200, 4), (200, 8000, 8), (900, 800, 4)):
+    m = mua.Muon(rows, cols, bits=bits)
+    x = torch.randn(m.d, generator=torch.Generator().manual_seed(rows)).cuda()
+    jobs.append((m, x, m.new_state(), m.new_workspace(), torch.zeros(m.d, device="cuda"),
+                 torch.empty(m.d, device="cuda"), torch.empty(rows, cols, device="cuda").bfloat16()))
+
+def run(m, x, st, ws, p, u, out):
+    m.step(p, x, st, ws, lr=0.1, t=1, seed=3)
+    m.momentum(x, st, u, beta=0.9, t=2, seed=3)
+    m.read_momentum(st, u)
+    m.write_momentum(u, st)
+    m.orthogonalize(u.view(m.rows, m.cols), out, ws)
+
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    for job in jobs:
+        run(*job)
+graph.replay()
+torch.cuda.synchronize()
+for m, x, st, ws, p, u, out in jobs:
+    twin = (m, x, m.new_state(), m.new_workspace(), torch.zeros_like(p), torch.empty_like(u),
+            torch.empty_like(out))
+    run(*twin)
+    for a, b in zip((st, p, u, out), (twin[2], twin[4], twin[5], twin[6])):
+        assert torch.equal(a, b)
+    assert m.status(st) == 0 and m.status(ws) == 0
+"""
+
+
+def test_first_calls_inside_a_capture(mua):
+    """In a process of its own, so that nothing has run before."""
+    r = subprocess.run([sys.executable, "-c", _FIRST_IN_A_CAPTURE.format(root=ROOT)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("rows,cols", [(1 << 15, 1 << 15), (1 << 20, 2047), (2047, 1 << 20)])
+def test_largest_shapes(mua, rows, cols):
+    """A scaled partial permutation: X_5 has the polynomial of each singular value
+    in the place of its entry and zeros elsewhere, so that no tile may go astray."""
+    s = min(rows, cols)
+    m = mua.Muon(rows, cols)
+    ws = m.new_workspace()
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    d = (torch.rand(s, generator=gen, device="cuda") * 0.5 + 0.5).to(torch.bfloat16)
+    far = torch.randperm(max(rows, cols), generator=gen, device="cuda")[:s]
+    near = torch.arange(s, device="cuda")
+    at = (near, far) if rows <= cols else (far, near)
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[at] = d
+    out = torch.full_like(x, 7.0)
+    m.orthogonalize(x, out, ws)
+    assert m.status(ws) == 0
+    want = d.double() / (d.double().norm() + 1e-7)
+    for _ in range(5):
+        a, b, c = muon_ref.QUINTIC
+        want = want * (a + want ** 2 * (b + want ** 2 * c))
+    assert int(torch.count_nonzero(out)) == s
+    # X, P and A's part in P are rounded once a step, at most 2^-11 each; the relative
+    # slopes of the last two steps multiply an early one by 8 at most.
+    assert bool(((out[at].double() - want).abs() <= 8 * 15 * 2.0 ** -11 * want.abs()).all())
