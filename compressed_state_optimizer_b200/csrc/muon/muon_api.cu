@@ -1,8 +1,8 @@
 // Host side of the mua_muon_* entry points declared in include/mua.h.
 //
 // A handle holds geometry and the polynomial's plan only. A step runs the
-// stack in groups of matrices (their X, A and P together stay near the L2's
-// size) and enqueues, per group: the norm of the direction, the momentum update
+// stack in groups of matrices (one X of a group takes at most kGroupBytes, half of
+// the L2; both X, A and P together may be more) and enqueues, per group: the norm of the direction, the momentum update
 // with X_0, and the Newton-Schulz steps in one launch whose last product
 // updates the parameters. No device memory is allocated and nothing is synchronized.
 #include <algorithm>
